@@ -641,6 +641,74 @@ pgf8_status pgf8_nestedfp_linear_group(const pgf8_nested_layer *layers, int64_t 
                                        void *stream);
 
 /* ------------------------------------------------------------------------
+ * E4M3 quantisation with block scales: the per-row rule of
+ * pgf8_fp8_quantize_rows (DYNAMIC) on blocks of 128 columns, so that an
+ * outlier costs resolution in its own block only.  The pages name per-tensor,
+ * per-token and per-channel scales ("C++ and FP8" §4.2); block scales are the
+ * next finer step, the form in which 8-bit checkpoints of large models store
+ * their weights.
+ *
+ * pgf8_fp8_quantize_blocks: x [batch, rows, cols] f32, f16 or bf16 (row
+ *   stride ldx, matrix stride ldb elements; ldb is ignored for batch <= 1).
+ *     block_rows 1    scales [batch * rows, ceil(cols / 128)]: one per 1 x 128
+ *                     group of a row (activations).  batch > 1 needs ldb ==
+ *                     rows * ldx (else UNSUPPORTED).
+ *     block_rows 128  scales [batch, ceil(rows / 128), ceil(cols / 128)]: one
+ *                     per 128 x 128 block (weights).
+ *   Blocks at the right and lower edges are the smaller rest.  Per block:
+ *   amax = max |x| (NaN ignored), s = fl32(amax / 448), 1 when that is 0;
+ *   code = E4M3 of fl32(x / s), nearest-even, saturating; a NaN gives the
+ *   NaN code; in a block with an infinity the scale is infinite, finite
+ *   values get zero codes and infinities the NaN code.  Bit-exact with respect
+ *   to that definition.  q [batch, rows, cols] contiguous.
+ * pgf8_fp8_silu_mul_quantize_blocks: gu [rows, 2*inter] f32, f16 or bf16 (row
+ *   stride ldg >= 2*inter; gate = columns [0, inter), up = [inter, 2*inter)):
+ *   h = gate / (1 + exp(-gate)) * up in binary32 is quantised with one scale
+ *   per 1 x 128 group: q [rows, inter], scales [rows, ceil(inter / 128)].
+ * Both: cols (inter) >= 16, a multiple of 16; x and q 16-byte aligned, row
+ * and matrix strides multiples of 16 bytes, scales 4-byte aligned.  No rows
+ * (or batch 0): no-op, pointers may be NULL.  flags:
+ * PGF8_FLAG_OVERLAP_PREVIOUS (nothing is read or written before the previous
+ * kernel in the stream has completed).
+ * ---------------------------------------------------------------------- */
+pgf8_status pgf8_fp8_quantize_blocks(const void *x, pgf8_dtype xdt, int64_t batch, int64_t rows, int64_t cols,
+                                     int64_t ldx, int64_t ldb, int32_t block_rows, uint8_t *q, float *scales,
+                                     int32_t flags, void *stream);
+pgf8_status pgf8_fp8_silu_mul_quantize_blocks(const void *gu, pgf8_dtype gdt, int64_t rows, int64_t inter,
+                                              int64_t ldg, uint8_t *q, float *scales, int32_t flags, void *stream);
+
+/* ------------------------------------------------------------------------
+ * FP8 linear layer with block scales:
+ *   y[m,n] = RN( sum_b sa[m,b] * sw[n / 128, b] *
+ *                sum_{k in block b} e4m3(aq[m,k]) * e4m3(wq[n,k]) )
+ * aq [M,K] codes with sa [M, ceil(K/128)] (one scale per 1 x 128 group),
+ * wq [N,K] codes with sw [ceil(N/128), ceil(K/128)] (one per 128 x 128
+ * block), as pgf8_fp8_quantize_blocks writes them; y [M,N] contiguous, ydt f32,
+ * f16 or bf16.  The products of a block and the sum over blocks are
+ * accumulated in binary32 and rounded once to ydt.  Scales may be any finite
+ * values.  0 <= M <= 2^23 (M == 0: no-op); K % 16 == 0, N % 16 == 0, any
+ * relation of K and N to 128.  aq, wq and y 16-byte aligned.  No workspace;
+ * calls on different streams may run at once.  Deterministic.
+ *
+ * pgf8_fp8_block_linear: quantised activations.  PGF8_FLAG_OVERLAP_PREVIOUS
+ *   as for pgf8_fp8_linear_ex.
+ * pgf8_fp8_block_linear_dynamic: x [M,K] f32, f16 or bf16 (row stride ldx)
+ *   is quantised per 1 x 128 group into the workspace (codes at offset 0,
+ *   scales at pgf8_fp8_block_linear_dynamic_scales_offset) by a first launch
+ *   that the GEMM's weight loads overlap.  workspace:
+ *   pgf8_fp8_block_linear_dynamic_workspace_size(M, K) bytes, 16-byte
+ *   aligned, not read before it is written (no zero-fill); one call at a
+ *   time may use it.
+ * ---------------------------------------------------------------------- */
+pgf8_status pgf8_fp8_block_linear(const uint8_t *aq, const float *sa, int64_t M, int64_t K, const uint8_t *wq,
+                                  const float *sw, int64_t N, void *y, pgf8_dtype ydt, int32_t flags, void *stream);
+pgf8_status pgf8_fp8_block_linear_dynamic(const void *x, pgf8_dtype xdt, int64_t M, int64_t K, int64_t ldx,
+                                          const uint8_t *wq, const float *sw, int64_t N, void *y, pgf8_dtype ydt,
+                                          void *workspace, size_t workspace_bytes, int32_t flags, void *stream);
+size_t pgf8_fp8_block_linear_dynamic_workspace_size(int64_t M, int64_t K);
+size_t pgf8_fp8_block_linear_dynamic_scales_offset(int64_t M, int64_t K);
+
+/* ------------------------------------------------------------------------
  * Allocation-free dynamic FP8 linear.  The pages have no counterpart of this
  * entry point; it exists for callers that cannot hand the library a
  * workspace: a host program that links only this C library and has no

@@ -111,6 +111,13 @@ _SIGS = {
     "pgf8_nestedfp_linear_group": ([ctypes.POINTER(NestedLayer), _i64, _i32, _vp, _sz, _optp, _vp], _i32),
     "pgf8_nestedfp_linear_workspace_size": ([_i64, _i64, _i64, _i32], _sz),
     "pgf8_fp8_linear_dynamic_noalloc": ([_vp, _i32, _i64, _i64, _i64, _vp, _vp, _i64, _vp, _vp], _i32),
+    "pgf8_fp8_quantize_blocks": ([_vp, _i32, _i64, _i64, _i64, _i64, _i64, _i32, _vp, _vp, _i32, _vp], _i32),
+    "pgf8_fp8_silu_mul_quantize_blocks": ([_vp, _i32, _i64, _i64, _i64, _vp, _vp, _i32, _vp], _i32),
+    "pgf8_fp8_block_linear": ([_vp, _vp, _i64, _i64, _vp, _vp, _i64, _vp, _i32, _i32, _vp], _i32),
+    "pgf8_fp8_block_linear_dynamic": ([_vp, _i32, _i64, _i64, _i64, _vp, _vp, _i64, _vp, _i32, _vp, _sz, _i32, _vp],
+                                      _i32),
+    "pgf8_fp8_block_linear_dynamic_workspace_size": ([_i64, _i64], _sz),
+    "pgf8_fp8_block_linear_dynamic_scales_offset": ([_i64, _i64], _sz),
     "pgf8_last_cuda_error": ([ctypes.POINTER(ctypes.c_int)], _i32),
     "pgf8_device_status": ([_vp], _i32),
     "pgf8_selftest_bounded_wait": ([_i64, _vp], _i32),
@@ -760,6 +767,188 @@ class NestedLayerGroup:
         _check(lib.pgf8_nestedfp_linear_group(self._arr, self.count, self.mode, _ptr(self.group_workspace),
                                               _nbytes(self.group_workspace), _opts(flags=flags), _stream(stream)),
                "nestedfp_linear_group")
+
+
+# ----------------------------------------------------------------- block scales
+_DTYPES = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
+
+
+class _On:
+    """Makes the device of a call's tensors and its stream current for as long
+    as the call's buffers are allocated and its work enqueued, so that memory
+    that is freed on return is only reused behind that work; yields the stream's
+    handle."""
+
+    __slots__ = ("dev", "stream", "outer_dev", "outer_stream")
+
+    def __init__(self, device, stream, *tensors):
+        if device.type != "cuda":
+            raise ValueError("pgf8 takes device tensors")
+        for t in tensors:
+            if t is not None and t.device != device:
+                raise ValueError(f"tensors on {t.device} and {device}: one call's tensors share a device")
+        self.dev, self.stream = device.index, stream
+
+    def __enter__(self):
+        self.outer_dev = torch.cuda.current_device()
+        self.outer_stream = None
+        if self.dev != self.outer_dev:
+            torch.cuda.set_device(self.dev)
+        try:
+            if self.stream is None:
+                return torch.cuda.current_stream().cuda_stream
+            stream = self.stream
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(int(stream), device=self.dev)
+            elif stream.device.index != self.dev:
+                raise ValueError(f"stream of {stream.device} for tensors on cuda:{self.dev}")
+            self.outer_stream = torch.cuda.current_stream()
+            torch.cuda.set_stream(stream)
+            return stream.cuda_stream
+        except BaseException:
+            self.__exit__()
+            raise
+
+    def __exit__(self, *exc):
+        if self.outer_stream is not None:
+            torch.cuda.set_stream(self.outer_stream)
+        if self.dev != self.outer_dev:
+            torch.cuda.set_device(self.outer_dev)
+
+
+def _code(dtype, what: str) -> int:
+    code = _DTYPES.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported {what} dtype {dtype}")
+    return code
+
+
+def _blocks(n: int) -> int:
+    return (n + 127) // 128
+
+
+def _want(t: torch.Tensor, shape: tuple, dtype, what: str):
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {shape}, not {t.dtype} "
+                         f"{tuple(t.shape)}")
+
+
+def fp8_quantize_blocks(x: torch.Tensor, block_rows: int = 1, q: torch.Tensor | None = None,
+                        scales: torch.Tensor | None = None, flags: int = 0, stream=None):
+    """E4M3 quantisation of x [rows, cols] or [batch, rows, cols] (f32, f16,
+    bf16; rows and matrices may be strided) with one scale per 1 x 128 group of
+    a row (block_rows 1: activations) or per 128 x 128 block (block_rows 128:
+    weights).  Returns (q uint8 of x's shape, scales f32 [.., ceil(rows /
+    block_rows), ceil(cols / 128)])."""
+    if x.dim() not in (2, 3) or block_rows not in (1, 128):
+        raise ValueError("x must be [rows, cols] or [batch, rows, cols], block_rows 1 or 128")
+    rows, cols = x.shape[-2:]
+    batch = x.shape[0] if x.dim() == 3 else 1
+    if cols > 1 and x.stride(-1) != 1:
+        raise ValueError("x rows must be contiguous")
+    # a dimension of one entry may carry any stride
+    ldx = x.stride(-2) if rows > 1 else max(cols, x.stride(0) if x.dim() == 3 and block_rows == 1 else 0)
+    ldb = x.stride(0) if batch > 1 else rows * ldx
+    code = _code(x.dtype, "x")
+    shape = (*x.shape[:-2], (rows + block_rows - 1) // block_rows, _blocks(cols))
+    with _On(x.device, stream, q, scales) as handle:
+        if q is None:
+            q = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
+        else:
+            _want(q, tuple(x.shape), torch.uint8, "q")
+        if scales is None:
+            scales = torch.empty(shape, dtype=torch.float32, device=x.device)
+        else:
+            _want(scales, shape, torch.float32, "scales")
+        _check(lib.pgf8_fp8_quantize_blocks(x.data_ptr(), code, batch, rows, cols, ldx, ldb, block_rows,
+                                            q.data_ptr(), scales.data_ptr(), flags, handle), "fp8_quantize_blocks")
+    return q, scales
+
+
+def fp8_silu_mul_quantize_blocks(gu: torch.Tensor, q: torch.Tensor | None = None,
+                                 scales: torch.Tensor | None = None, flags: int = 0, stream=None):
+    """silu(gate) * up of the gate+up output gu [rows, 2I] (f32, f16 or bf16;
+    gate = first I columns), quantised to E4M3 with one scale per 1 x 128
+    group.  Returns (q uint8 [rows, I], scales f32 [rows, ceil(I / 128)])."""
+    if gu.dim() != 2 or gu.stride(1) != 1 or gu.shape[1] % 2:
+        raise ValueError("gu must be [rows, 2I] with contiguous rows")
+    rows, inter = gu.shape[0], gu.shape[1] // 2
+    code = _code(gu.dtype, "gate/up")
+    with _On(gu.device, stream, q, scales) as handle:
+        if q is None:
+            q = torch.empty((rows, inter), dtype=torch.uint8, device=gu.device)
+        else:
+            _want(q, (rows, inter), torch.uint8, "q")
+        if scales is None:
+            scales = torch.empty((rows, _blocks(inter)), dtype=torch.float32, device=gu.device)
+        else:
+            _want(scales, (rows, _blocks(inter)), torch.float32, "scales")
+        _check(lib.pgf8_fp8_silu_mul_quantize_blocks(gu.data_ptr(), code, rows, inter, _lead(gu), q.data_ptr(),
+                                                     scales.data_ptr(), flags, handle),
+               "fp8_silu_mul_quantize_blocks")
+    return q, scales
+
+
+def _block_weights(wq, sw, K):
+    if wq.dim() != 2 or wq.shape[1] != K:
+        raise ValueError(f"wq must be [N, {K}]")
+    _want(wq, tuple(wq.shape), torch.uint8, "wq")
+    _want(sw, (_blocks(wq.shape[0]), _blocks(K)), torch.float32, "sw")
+    return wq.shape[0]
+
+
+def _block_out(y, shape, out_dtype, device):
+    if y is None:
+        return torch.empty(shape, dtype=out_dtype, device=device), _code(out_dtype, "output")
+    _want(y, shape, y.dtype, "y")
+    return y, _code(y.dtype, "output")
+
+
+def fp8_block_linear(aq: torch.Tensor, sa: torch.Tensor, wq: torch.Tensor, sw: torch.Tensor,
+                     y: torch.Tensor | None = None, out_dtype: torch.dtype = torch.bfloat16, flags: int = 0,
+                     stream=None) -> torch.Tensor:
+    """y [M, N] (f32, f16 or bf16: y's type, or out_dtype) of E4M3 activations
+    aq [M, K] with scales sa [M, ceil(K / 128)] and E4M3 weights wq [N, K] with
+    scales sw [ceil(N / 128), ceil(K / 128)], as fp8_quantize_blocks gives them."""
+    if aq.dim() != 2:
+        raise ValueError("aq must be [M, K]")
+    M, K = aq.shape
+    _want(aq, (M, K), torch.uint8, "aq")
+    _want(sa, (M, _blocks(K)), torch.float32, "sa")
+    N = _block_weights(wq, sw, K)
+    with _On(aq.device, stream, sa, wq, sw, y) as handle:
+        y, code = _block_out(y, (M, N), out_dtype, aq.device)
+        _check(lib.pgf8_fp8_block_linear(aq.data_ptr(), sa.data_ptr(), M, K, wq.data_ptr(), sw.data_ptr(), N,
+                                         y.data_ptr(), code, flags, handle), "fp8_block_linear")
+    return y
+
+
+def fp8_block_linear_dynamic(x: torch.Tensor, wq: torch.Tensor, sw: torch.Tensor, y: torch.Tensor | None = None,
+                             out_dtype: torch.dtype = torch.bfloat16, workspace: torch.Tensor | None = None,
+                             flags: int = 0, stream=None) -> torch.Tensor:
+    """fp8_block_linear of x [M, K] (f32, f16 or bf16; rows may be strided),
+    quantised in the call with one scale per 1 x 128 group.  Without a workspace
+    (fp8_block_linear_dynamic_workspace_size bytes) the call allocates one, on
+    its stream."""
+    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
+        raise ValueError("x must be [M, K] with contiguous rows")
+    M, K = x.shape
+    xcode = _code(x.dtype, "activation")
+    N = _block_weights(wq, sw, K)
+    with _On(x.device, stream, wq, sw, y, workspace) as handle:
+        y, code = _block_out(y, (M, N), out_dtype, x.device)
+        if workspace is None:
+            workspace = torch.empty(lib.pgf8_fp8_block_linear_dynamic_workspace_size(M, K), dtype=torch.uint8,
+                                    device=x.device)
+        _check(lib.pgf8_fp8_block_linear_dynamic(x.data_ptr(), xcode, M, K, _lead(x) if M else K, wq.data_ptr(),
+                                                 sw.data_ptr(), N, y.data_ptr(), code, workspace.data_ptr(),
+                                                 _nbytes(workspace), flags, handle), "fp8_block_linear_dynamic")
+    return y
+
+
+def fp8_block_linear_dynamic_workspace_size(M: int, K: int) -> int:
+    """Workspace bytes of fp8_block_linear_dynamic (no zero-fill needed)."""
+    return int(lib.pgf8_fp8_block_linear_dynamic_workspace_size(M, K))
 
 
 def selftest_row_division(divisors: torch.Tensor, stream=None):

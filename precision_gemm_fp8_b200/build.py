@@ -18,7 +18,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libpgf8.so")
 SOURCES = ["pgf8_api.cu"]
 DEPS = ["pgf8_api.cu", "gemm.cuh", "gemm_persistent.cuh", "gemm_streamk.cuh", "gemm_2sm.cuh", "gemm_group.cuh", "quantize.cuh", "sm100_ptx.cuh",
-        "kvcache.cuh", "attention.cuh", "attention_context.cuh"]
+        "kvcache.cuh", "attention.cuh", "attention_context.cuh", "gemm_pair_group.cuh", "gemm_persistent_swap.cuh",
+        "block_api.cuh", "gemm_block.cuh", "quantize_blocks.cuh", "packed_ptx.cuh"]
 
 
 def _nvcc() -> str:

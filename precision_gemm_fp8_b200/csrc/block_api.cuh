@@ -1,0 +1,281 @@
+// Entry points of the block-scaled FP8 operators (quantisation, gate, linear
+// layer); specified in include/pgf8.h.  Included by pgf8_api.cu after its
+// helpers.
+#pragma once
+
+#include "gemm_block.cuh"
+#include "quantize_blocks.cuh"
+
+namespace pgf8 {
+
+static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Bytes of an element, 0 for an unknown type.
+static int dtype_bytes(int dt)
+{
+    return dt == PGF8_F32 ? 4 : (dt == PGF8_F16 || dt == PGF8_BF16) ? 2 : 0;
+}
+
+// Calls f with a null pointer of the element type.
+template <class F> static pgf8_status by_dtype(int dt, F f)
+{
+    if (dt == PGF8_F32)
+        return f(static_cast<const float *>(nullptr));
+    if (dt == PGF8_F16)
+        return f(static_cast<const __half *>(nullptr));
+    return f(static_cast<const __nv_bfloat16 *>(nullptr));
+}
+
+static pgf8_status check_block_quant(const void *x, int xdt, int64_t batch, int64_t rows, int64_t cols, int64_t ldx,
+                                     int64_t ldb, int block_rows, const uint8_t *q, const float *scales)
+{
+    if (batch < 0 || rows < 0 || cols < 16 || cols > (1ll << 30) || ldx < cols || ldx > (1ll << 40) ||
+        rows > (1ll << 31) - 1 || batch > (1ll << 31) - 1 || (block_rows != 1 && block_rows != 128))
+        return PGF8_ERR_INVALID_ARG;
+    if (batch == 0 || rows == 0)
+        return PGF8_OK;
+    if (batch > 1 && (ldb < 0 || ldb > (1ll << 50)))
+        return PGF8_ERR_INVALID_ARG;
+    if (!x || !q || !scales)
+        return PGF8_ERR_INVALID_ARG;
+    const int eb = dtype_bytes(xdt);
+    if (eb == 0)
+        return PGF8_ERR_UNSUPPORTED;
+    if (cols % 16 != 0 || (ldx * eb) % 16 != 0 || (batch > 1 && (ldb * eb) % 16 != 0) || !aligned16(x) ||
+        !aligned16(q) || !aligned4(scales))
+        return PGF8_ERR_ALIGNMENT;
+    // one launch: the grid's x extent holds every CTA (8 threads a row group, a CTA a tile)
+    const int64_t cb = ceil_div(cols, 128);
+    const double ctas = block_rows == 1 ? static_cast<double>(batch) * rows * cb / 32
+                                        : static_cast<double>(batch) * ceil_div(rows, 128) * cb;
+    if (ctas > 2147483000.0)
+        return PGF8_ERR_UNSUPPORTED;
+    return PGF8_OK;
+}
+
+// 1 x 128 groups of rows (arguments checked, rows > 0).
+static pgf8_status row_blocks_launch(const void *x, int xdt, int64_t rows, int64_t cols, int64_t ldx, uint8_t *q,
+                                     float *scales, cudaStream_t cs, int pdl)
+{
+    const int64_t groups = ceil_div(cols, 128);
+    const uint64_t total = static_cast<uint64_t>(rows) * static_cast<uint64_t>(groups);
+    const unsigned grid = static_cast<unsigned>((total + 31) / 32);
+    return by_dtype(xdt, [&](auto *t) {
+        using T = std::remove_cv_t<std::remove_pointer_t<decltype(t)>>;
+        return launch_quant(quantize_row_blocks_kernel<T>, grid, cs, pdl, static_cast<const T *>(x), total,
+                            static_cast<uint32_t>(groups), cols, ldx, q, scales);
+    });
+}
+
+// ------------------------------------------------------------------ linear
+struct BlockLaunch {
+    const uint8_t *aq, *wq;
+    const float *sa, *sw;
+    void *y;
+    int ydt;
+    int64_t M, N, K;
+    int prefetch_w;
+    cudaStream_t stream;
+};
+
+// K-split of the weight-streaming kernel: the largest cluster that keeps the
+// grid within `slots` CTAs (all of them resident at once, so that none waits
+// for a second round while the others hold the memory system) and leaves at
+// least four k-blocks to a CTA.
+static int block_splits(int64_t tiles, int64_t kblocks, int64_t slots)
+{
+    static const int kSizes[] = {8, 6, 4, 3, 2};
+    for (int s : kSizes)
+        if (tiles * s <= slots && kblocks >= 4 * s)
+            return s;
+    return 1;
+}
+
+template <class C> static pgf8_status launch_block(const BlockLaunch &L, int ctas_per_sm)
+{
+    static PerDeviceSetup setup;
+    const cudaError_t attr_err = setup_once_per_device(setup, [](int, int *) {
+        cudaError_t e = cudaFuncSetAttribute(gemm_block_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             C::kSmemBytes);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(gemm_block_kernel<C>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                     cudaSharedmemCarveoutMaxShared);
+        return e;
+    });
+    if (attr_err != cudaSuccess)
+        return cuda_fail(attr_err);
+    CUtensorMap tmX, tmW;
+    if (!make_map(&tmX, L.aq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, L.M, L.K, 128, C::BN, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !make_map(&tmW, L.wq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, L.N, L.K, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B))
+        return PGF8_ERR_UNSUPPORTED;
+    BlockParams p;
+    p.M = static_cast<int>(L.M);
+    p.N = static_cast<int>(L.N);
+    p.K = static_cast<int>(L.K);
+    p.kblocks = static_cast<int>(ceil_div(L.K, 128));
+    p.prefetch_w = L.prefetch_w;
+    p.sa = L.sa;
+    p.sw = L.sw;
+    p.y = L.y;
+    p.ydt = L.ydt;
+    const int64_t nt = ceil_div(L.N, 128), mt = ceil_div(L.M, C::BN);
+    if (mt > 65535)
+        return PGF8_ERR_UNSUPPORTED;   // the grid's y extent
+    const int splits = block_splits(nt * mt, p.kblocks, static_cast<int64_t>(ctas_per_sm) * num_sms());
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = dim3(static_cast<unsigned>(nt), static_cast<unsigned>(mt), static_cast<unsigned>(splits));
+    cfg.blockDim = dim3(C::kThreads, 1, 1);
+    cfg.dynamicSmemBytes = C::kSmemBytes;
+    cfg.stream = L.stream;
+    cudaLaunchAttribute attrs[2];
+    fill_attrs(cfg, attrs, splits, 1);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, gemm_block_kernel<C>, tmX, tmW, p);
+    return e == cudaSuccess ? PGF8_OK : cuda_fail(e);
+}
+
+static pgf8_status block_linear_launch(const BlockLaunch &L)
+{
+    if (L.M <= 16)
+        return launch_block<BlockCfg<16, 6, 4>>(L, 2);
+    if (L.M <= 32)
+        return launch_block<BlockCfg<32, 5, 4>>(L, 2);
+    if (L.M <= 64)
+        return launch_block<BlockCfg<64, 4, 4>>(L, 2);
+    return launch_block<BlockCfg<128, 6, 4>>(L, 1);
+}
+
+// Shapes, types and pointers of a block-scaled linear layer, activations aside.
+static pgf8_status check_block_linear(int64_t M, int64_t K, const uint8_t *wq, const float *sw, int64_t N,
+                                      const void *y, int ydt)
+{
+    if (M < 0 || N < 16 || K < 16 || M > (1ll << 23) || N > (1ll << 30) || K > (1ll << 30))
+        return PGF8_ERR_INVALID_ARG;
+    if (K % 16 != 0 || N % 16 != 0)
+        return PGF8_ERR_ALIGNMENT;
+    if (M == 0)
+        return PGF8_OK;
+    if (!wq || !sw || !y)
+        return PGF8_ERR_INVALID_ARG;
+    if (dtype_bytes(ydt) == 0)
+        return PGF8_ERR_UNSUPPORTED;
+    if (!aligned16(wq) || !aligned16(y) || !aligned4(sw))
+        return PGF8_ERR_ALIGNMENT;
+    return PGF8_OK;
+}
+
+static size_t block_scales_offset(int64_t M, int64_t K)
+{
+    return round_up(static_cast<size_t>(M) * static_cast<size_t>(K), 256);
+}
+
+} // namespace pgf8
+
+using namespace pgf8;
+
+extern "C" {
+
+pgf8_status pgf8_fp8_quantize_blocks(const void *x, pgf8_dtype xdt, int64_t batch, int64_t rows, int64_t cols,
+                                     int64_t ldx, int64_t ldb, int32_t block_rows, uint8_t *q, float *scales,
+                                     int32_t flags, void *stream)
+{
+    pgf8_status st = check_block_quant(x, xdt, batch, rows, cols, ldx, ldb, block_rows, q, scales);
+    if (st != PGF8_OK)
+        return st;
+    if (batch == 0 || rows == 0)
+        return PGF8_OK;
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    const int pdl = (flags & PGF8_FLAG_OVERLAP_PREVIOUS) ? 1 : 0;
+    if (block_rows == 1) {
+        if (batch > 1) {
+            // the matrices' rows as one list: they have to follow one another
+            if (ldb != rows * ldx)
+                return PGF8_ERR_UNSUPPORTED;
+            rows *= batch;
+        }
+        return row_blocks_launch(x, xdt, rows, cols, ldx, q, scales, cs, pdl);
+    }
+    const uint32_t rb = static_cast<uint32_t>(ceil_div(rows, 128)), cb = static_cast<uint32_t>(ceil_div(cols, 128));
+    const unsigned grid = static_cast<unsigned>(batch * rb * cb);
+    return by_dtype(xdt, [&](auto *t) {
+        using T = std::remove_cv_t<std::remove_pointer_t<decltype(t)>>;
+        return launch_quant(quantize_tiles_kernel<T>, grid, cs, pdl, static_cast<const T *>(x), rows, cols, ldx, ldb,
+                            rb, cb, q, scales);
+    });
+}
+
+pgf8_status pgf8_fp8_silu_mul_quantize_blocks(const void *gu, pgf8_dtype gdt, int64_t rows, int64_t inter,
+                                              int64_t ldg, uint8_t *q, float *scales, int32_t flags, void *stream)
+{
+    if (inter < 0 || inter > (1ll << 30) || ldg < 2 * inter)
+        return PGF8_ERR_INVALID_ARG;
+    pgf8_status st = check_block_quant(gu, gdt, 1, rows, inter, ldg, 0, 1, q, scales);
+    if (st != PGF8_OK)
+        return st;
+    if (rows == 0)
+        return PGF8_OK;
+    const int64_t groups = ceil_div(inter, 128);
+    const uint64_t total = static_cast<uint64_t>(rows) * static_cast<uint64_t>(groups);
+    const unsigned grid = static_cast<unsigned>((total + 31) / 32);
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    const int pdl = (flags & PGF8_FLAG_OVERLAP_PREVIOUS) ? 1 : 0;
+    return by_dtype(gdt, [&](auto *t) {
+        using T = std::remove_cv_t<std::remove_pointer_t<decltype(t)>>;
+        return launch_quant(silu_mul_row_blocks_kernel<T>, grid, cs, pdl, static_cast<const T *>(gu), total,
+                            static_cast<uint32_t>(groups), inter, ldg, q, scales);
+    });
+}
+
+pgf8_status pgf8_fp8_block_linear(const uint8_t *aq, const float *sa, int64_t M, int64_t K, const uint8_t *wq,
+                                  const float *sw, int64_t N, void *y, pgf8_dtype ydt, int32_t flags, void *stream)
+{
+    pgf8_status st = check_block_linear(M, K, wq, sw, N, y, ydt);
+    if (st != PGF8_OK || M == 0)
+        return st;
+    if (!aq || !sa)
+        return PGF8_ERR_INVALID_ARG;
+    if (!aligned16(aq) || !aligned4(sa))
+        return PGF8_ERR_ALIGNMENT;
+    BlockLaunch L = {aq, wq, sa, sw, y, ydt, M, N, K, (flags & PGF8_FLAG_OVERLAP_PREVIOUS) ? 1 : 0,
+                     static_cast<cudaStream_t>(stream)};
+    return block_linear_launch(L);
+}
+
+size_t pgf8_fp8_block_linear_dynamic_scales_offset(int64_t M, int64_t K)
+{
+    return M < 0 || K < 0 ? 0 : block_scales_offset(M, K);
+}
+
+size_t pgf8_fp8_block_linear_dynamic_workspace_size(int64_t M, int64_t K)
+{
+    if (M <= 0 || K <= 0)
+        return 0;
+    return block_scales_offset(M, K) + round_up(static_cast<size_t>(M) * ceil_div(K, 128) * 4, 256);
+}
+
+pgf8_status pgf8_fp8_block_linear_dynamic(const void *x, pgf8_dtype xdt, int64_t M, int64_t K, int64_t ldx,
+                                          const uint8_t *wq, const float *sw, int64_t N, void *y, pgf8_dtype ydt,
+                                          void *workspace, size_t workspace_bytes, int32_t flags, void *stream)
+{
+    pgf8_status st = check_block_linear(M, K, wq, sw, N, y, ydt);
+    if (st != PGF8_OK || M == 0)
+        return st;
+    if (!workspace || workspace_bytes < pgf8_fp8_block_linear_dynamic_workspace_size(M, K))
+        return PGF8_ERR_INVALID_ARG;
+    if (!aligned16(workspace))
+        return PGF8_ERR_ALIGNMENT;
+    uint8_t *aq = static_cast<uint8_t *>(workspace);
+    float *sa = reinterpret_cast<float *>(aq + block_scales_offset(M, K));
+    st = check_block_quant(x, xdt, 1, M, K, ldx, 0, 1, aq, sa);
+    if (st != PGF8_OK)
+        return st;
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    st = row_blocks_launch(x, xdt, M, K, ldx, aq, sa, cs, (flags & PGF8_FLAG_OVERLAP_PREVIOUS) ? 1 : 0);
+    if (st != PGF8_OK)
+        return st;
+    // the quantisation writes only aq / sa: weights may be read while it runs
+    BlockLaunch L = {aq, wq, sa, sw, y, ydt, M, N, K, 1, cs};
+    return block_linear_launch(L);
+}
+
+} // extern "C"

@@ -1,0 +1,369 @@
+// FP8 linear layer with block scales, weights as the 128-row MMA operand:
+//   y[m, n] = sum_b sa[m, b] sw[n / 128, b] sum_{k in block b} a[m, k] w[n, k]
+// with blocks of 128 along K (E4M3 codes, scales f32).
+//
+// The scales vary along K, so the tensor core cannot add the blocks up
+// itself: tcgen05 accumulates one k-block (4 MMAs of 32 bytes of K) in tensor
+// memory in binary32, and the epilogue warps add it, times its scale, to the
+// output tile that they hold in registers, while the MMAs of the next
+// k-blocks fill the other accumulator buffers.  Per k-block and tile that is
+// one multiply-add an output; each is rounded once to binary32 (sums stay
+// in binary32 until the final rounding to the output type).
+//
+// For few tokens the layer is bound by the weight stream (N K bytes at HBM
+// speed), so the K range of a weight tile is split over a thread-block
+// cluster until the grid fills the GPU; the CTAs' partial tiles are added in
+// rank order through distributed shared memory (no workspace, the same
+// result in every run).
+//
+//   warp 0      TMA producer: STAGES-deep ring of (weight tile, token tile)
+//   warp 1      tensor-memory allocation, MMA issue (one thread)
+//   warps 2-5   scales, accumulation over k-blocks, output: thread r holds
+//               weight row r of the tile, BN tokens
+// Waits are bounded as in gemm.cuh; after a wait that gave up the epilogue
+// warps keep walking their loop without touching tensor memory, so that
+// their barriers stay matched.
+#pragma once
+
+#include "gemm.cuh"
+#include "packed_ptx.cuh"
+
+namespace pgf8 {
+
+constexpr int kScaleChunk = 8;   // k-blocks of token scales staged in shared memory at a time
+
+template <int BN_, int STAGES_, int NBUF_> struct BlockCfg {
+    static constexpr int BN = BN_;
+    static constexpr int STAGES = STAGES_;
+    static constexpr int NBUF = NBUF_;   // accumulator buffers of BN columns
+    static constexpr int KIND = kE4M3;
+    static constexpr int XQ = 0;
+    static constexpr int kThreads = 192;
+    static constexpr int kTileA = 128 * 128;
+    static constexpr int kStage = kTileA + BN * 128;
+    static constexpr int kRowsW = 128;
+    static constexpr int kRowsX = BN;
+    static constexpr int kTmemCols = NBUF * BN < 32 ? 32 : NBUF * BN;
+    static constexpr int kRingBytes = STAGES * kStage;   // reused for the partial tile [BN][128] f32
+    static constexpr int kScalePitch = BN + 4;           // floats; the 8 k-blocks' writes then hit distinct banks
+    static constexpr int kScaleOffset = kRingBytes;
+    static constexpr int kScaleBytes = 2 * kScaleChunk * kScalePitch * 4;
+    static constexpr int kCtlOffset = kScaleOffset + kScaleBytes;
+    static constexpr int kSmemBytes = kCtlOffset + 512 + 1024;
+    static_assert(BN == 16 || BN == 32 || BN == 64 || BN == 128, "token tile");
+    static_assert(STAGES <= 8 && NBUF <= 8, "barriers");
+    static_assert((kTmemCols & (kTmemCols - 1)) == 0 && kTmemCols <= 512, "tensor memory");
+    static_assert(kRingBytes >= BN * 128 * 4, "partial tile");
+    static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+};
+
+struct BlockCtl {
+    uint64_t full[8];
+    uint64_t empty[8];
+    uint64_t acc_full[8];
+    uint64_t acc_empty[8];
+    uint64_t drain;
+    uint32_t tmem_base;
+    int abort;
+};
+
+struct BlockParams {
+    int M, N, K, kblocks;
+    int prefetch_w;      // 1: weight tiles may be loaded before the grid dependency resolves
+    const float *sa;     // [M, kblocks]
+    const float *sw;     // [ceil(N / 128), kblocks]
+    void *y;             // [M, N]
+    int ydt;             // pgf8_dtype
+};
+
+// v rounded once to the output type.
+__device__ __forceinline__ void store_out(void *y, int64_t i, float v, int dt)
+{
+    if (dt == 2)
+        static_cast<__nv_bfloat16 *>(y)[i] = __float2bfloat16_rn(v);
+    else if (dt == 1)
+        static_cast<__half *>(y)[i] = __float2half_rn(v);
+    else
+        static_cast<float *>(y)[i] = v;
+}
+
+// Four consecutive outputs (the address is a multiple of four elements).
+__device__ __forceinline__ void store_out4(void *y, int64_t i, float4 v, int dt)
+{
+    if (dt == 2) {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(y) + i) =
+            make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+    } else if (dt == 1) {
+        const __half2 a = __floats2half2_rn(v.x, v.y), b = __floats2half2_rn(v.z, v.w);
+        *reinterpret_cast<uint2 *>(static_cast<__half *>(y) + i) =
+            make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+    } else {
+        *reinterpret_cast<float4 *>(static_cast<float *>(y) + i) = v;
+    }
+}
+
+// Adds accumulator columns [0, BN) of this thread's row (tensor memory at
+// taddr) times their scales (shared memory, 16-byte aligned) to acc.
+template <int BN>
+__device__ __forceinline__ void add_scaled(uint32_t taddr, const float *sc, uint64_t (&acc)[BN / 2])
+{
+    constexpr int W = BN < 32 ? 16 : 32;
+#pragma unroll
+    for (int c0 = 0; c0 < BN; c0 += W) {
+        uint32_t v[W];
+        if constexpr (W == 32)
+            tmem_ld_32x32b_x32(taddr + c0, v);
+        else
+            tmem_ld_32x32b_x16(taddr + c0, v);
+        tmem_ld_wait();
+        const ulonglong2 *s = reinterpret_cast<const ulonglong2 *>(sc + c0);
+#pragma unroll
+        for (int j = 0; j < W / 4; ++j) {
+            const ulonglong2 t = s[j];
+            acc[c0 / 2 + 2 * j] = fma_f32x2(pack_f32x2(v[4 * j], v[4 * j + 1]), t.x, acc[c0 / 2 + 2 * j]);
+            acc[c0 / 2 + 2 * j + 1] = fma_f32x2(pack_f32x2(v[4 * j + 2], v[4 * j + 3]), t.y,
+                                                acc[c0 / 2 + 2 * j + 1]);
+        }
+    }
+}
+
+template <class C>
+__global__ void __launch_bounds__(C::kThreads)
+    gemm_block_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
+                      const BlockParams p)
+{
+    constexpr int BN = C::BN, STAGES = C::STAGES, NBUF = C::NBUF;
+    grid_launch_dependents();
+
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    float *sc = reinterpret_cast<float *>(smem + C::kScaleOffset);
+    BlockCtl *ctl = reinterpret_cast<BlockCtl *>(smem + C::kCtlOffset);
+    volatile int *abort_flag = &ctl->abort;
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const int n0 = static_cast<int>(blockIdx.x) * 128;
+    const int m0 = static_cast<int>(blockIdx.y) * BN;
+    const int splits = static_cast<int>(gridDim.z);   // the cluster along z
+    const int kb0 = static_cast<int>(static_cast<int64_t>(p.kblocks) * blockIdx.z / splits);
+    const int kb1 = static_cast<int>(static_cast<int64_t>(p.kblocks) * (blockIdx.z + 1) / splits);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&ctl->full[s], 1);
+            mbar_init(&ctl->empty[s], 1);
+        }
+        for (int b = 0; b < NBUF; ++b) {
+            mbar_init(&ctl->acc_full[b], 1);
+            mbar_init(&ctl->acc_empty[b], 4);
+        }
+        mbar_init(&ctl->drain, 1);
+        ctl->abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(&ctl->tmem_base, C::kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = ctl->tmem_base;
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ producer
+        if (lane == 0) {
+            const uint64_t pol_w = policy_evict_first();
+            const uint64_t pol_x = policy_evict_last();
+            if (!p.prefetch_w)
+                grid_dependency_wait();
+            // the first ring pass: weights at once, token tiles after the dependency
+            const int first = kb1 - kb0 < STAGES ? kb1 - kb0 : STAGES;
+            for (int i = 0; i < first; ++i) {
+                mbar_arrive_expect_tx(&ctl->full[i], C::kStage);
+                tma_load_2d_hint(smem + i * C::kStage, &tmW, &ctl->full[i], (kb0 + i) * 128, n0, pol_w);
+            }
+            if (p.prefetch_w)
+                grid_dependency_wait();
+            for (int i = 0; i < first; ++i)
+                tma_load_2d_hint(smem + i * C::kStage + C::kTileA, &tmX, &ctl->full[i], (kb0 + i) * 128, m0, pol_x);
+            int s = 0;
+            uint32_t ph = 0;
+            int issued = first;
+            for (int kb = kb0 + first; kb < kb1; ++kb) {
+                if (!wait_bounded(&ctl->empty[s], ph, abort_flag))
+                    break;
+                uint8_t *st = smem + s * C::kStage;
+                mbar_arrive_expect_tx(&ctl->full[s], C::kStage);
+                tma_load_2d_hint(st, &tmW, &ctl->full[s], kb * 128, n0, pol_w);
+                tma_load_2d_hint(st + C::kTileA, &tmX, &ctl->full[s], kb * 128, m0, pol_x);
+                ++issued;
+                if (++s == STAGES) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            }
+            if (*abort_flag) {
+                // the last load into each used stage lands (bounded) before the CTA may exit
+                for (int j = 0; j < STAGES && j < issued; ++j)
+                    wait_drain(&ctl->full[j], static_cast<uint32_t>((issued - 1 - j) / STAGES) & 1u);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer
+        grid_dependency_wait();
+        if (lane == 0) {
+            constexpr uint32_t idesc = make_idesc(128, BN, 0, 0);
+            int s = 0, b = 0;
+            uint32_t ph = 0, bph = 1;
+            bool ok = true;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!wait_bounded(&ctl->acc_empty[b], bph, abort_flag) ||
+                    !wait_bounded(&ctl->full[s], ph, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t a_addr = smem_u32(smem + s * C::kStage);
+                const uint32_t b_addr = a_addr + C::kTileA;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    umma_f8f6f4(tmem + b * BN, sdesc_sw128(a_addr + k * 32), sdesc_sw128(b_addr + k * 32), idesc,
+                                k > 0 ? 1u : 0u);
+                umma_commit(&ctl->empty[s]);
+                umma_commit(&ctl->acc_full[b]);
+                if (++s == STAGES) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+                if (++b == NBUF) {
+                    b = 0;
+                    bph ^= 1u;
+                }
+            }
+            if (!ok) {
+                umma_commit(&ctl->drain);
+                wait_drain(&ctl->drain, 0);
+            }
+        }
+        __syncwarp();
+    }
+
+    uint64_t acc[BN / 2];
+    const int qd = warp & 3;
+    const int r = qd * 32 + lane;
+    if (warp >= 2) {
+        // ------------------------------------------------------------ scales and accumulation
+        grid_dependency_wait();   // the token scales come from the kernel before
+#pragma unroll
+        for (int j = 0; j < BN / 2; ++j)
+            acc[j] = 0;
+        const uint32_t t_row = tmem + (static_cast<uint32_t>(qd * 32) << 16);
+        const int et = static_cast<int>(threadIdx.x) - 64;
+        // sa[m, kb] * sw[n0 / 128, kb] of 8 k-blocks from kb: thread et's values are
+        // tokens (et + 128 i) / 8 at k-block kb + et % 8 (32 contiguous bytes a token)
+        constexpr int PER = BN * kScaleChunk / 128;
+        float pre[PER];
+        const float *swr = p.sw + static_cast<int64_t>(blockIdx.x) * p.kblocks;
+        auto fetch = [&](int kb) {
+            const int k = kb + (et & 7);
+            const float w = k < kb1 ? __ldg(swr + k) : 0.0f;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const int m = m0 + ((et + 128 * i) >> 3);
+                pre[i] = (k < kb1 && m < p.M) ? p.sa[static_cast<int64_t>(m) * p.kblocks + k] * w : 0.0f;
+            }
+        };
+        fetch(kb0);
+        int b = 0;
+        uint32_t bph = 0;
+        bool ok = true;
+        for (int i = 0; i < kb1 - kb0; ++i) {
+            float *buf = sc + ((i / kScaleChunk) & 1) * kScaleChunk * C::kScalePitch;
+            if (i % kScaleChunk == 0) {
+#pragma unroll
+                for (int j = 0; j < PER; ++j)
+                    buf[(et & 7) * C::kScalePitch + ((et + 128 * j) >> 3)] = pre[j];
+                fetch(kb0 + i + kScaleChunk);
+                bar_sync_warps2to5();
+            }
+            ok = ok && wait_bounded(&ctl->acc_full[b], bph, abort_flag);
+            ok = __all_sync(0xffffffffu, ok);
+            if (ok) {
+                tc_fence_after();
+                add_scaled<BN>(t_row + b * BN, buf + (i % kScaleChunk) * C::kScalePitch, acc);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&ctl->acc_empty[b]);
+            }
+            if (++b == NBUF) {
+                b = 0;
+                bph ^= 1u;
+            }
+        }
+    }
+    __syncwarp();
+
+    // ---------------------------------------------------------------- output
+    const int n = n0 + r;
+    if (splits == 1) {
+        if (warp >= 2 && n < p.N) {
+#pragma unroll
+            for (int c = 0; c < BN; c += 2) {
+                const float2 v = unpack_f32x2(acc[c / 2]);
+                if (m0 + c < p.M)
+                    store_out(p.y, static_cast<int64_t>(m0 + c) * p.N + n, v.x, p.ydt);
+                if (m0 + c + 1 < p.M)
+                    store_out(p.y, static_cast<int64_t>(m0 + c + 1) * p.N + n, v.y, p.ydt);
+            }
+        }
+        tc_fence_before();
+        __syncthreads();
+    } else {
+        // partial tile [BN][128] over the idle ring; CTA z of the cluster finishes
+        // tokens z, z + splits, ... : the partials in rank order
+        float *part = reinterpret_cast<float *>(smem);
+        const int cols = p.M - m0 < BN ? p.M - m0 : BN;
+        tc_fence_before();
+        __syncthreads();
+        if (warp >= 2) {
+#pragma unroll
+            for (int c = 0; c < BN; c += 2) {
+                const float2 v = unpack_f32x2(acc[c / 2]);
+                part[c * 128 + r] = v.x;
+                part[(c + 1) * 128 + r] = v.y;
+            }
+        }
+        cluster_sync_all();
+        if (warp >= 2) {
+            // four weight rows a thread, so that a column's partials are in
+            // flight together and go out as one store
+            const int n4 = n0 + lane * 4;
+            const uint32_t base = smem_u32(part) + lane * 16;
+            for (int c = static_cast<int>(blockIdx.z) + splits * (warp - 2); n4 < p.N && c < cols; c += 4 * splits) {
+                float4 t[8];
+#pragma unroll
+                for (int z = 0; z < 8; ++z)
+                    if (z < splits)
+                        t[z] = ld_shared_cluster_v4_relaxed(map_shared_rank(base + c * 512, static_cast<uint32_t>(z)));
+                float4 v = t[0];
+#pragma unroll
+                for (int z = 1; z < 8; ++z)
+                    if (z < splits)
+                        v = make_float4(v.x + t[z].x, v.y + t[z].y, v.z + t[z].z, v.w + t[z].w);
+                store_out4(p.y, static_cast<int64_t>(m0 + c) * p.N + n4, v, p.ydt);
+            }
+        }
+        cluster_sync_all();   // no CTA leaves while its partial may still be read
+    }
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::kTmemCols);
+    }
+}
+
+} // namespace pgf8

@@ -7,6 +7,7 @@
 #include <cmath>
 #include <cstring>
 #include <mutex>
+#include <type_traits>
 
 #include "pgf8.h"
 #include "gemm.cuh"
@@ -2580,3 +2581,6 @@ pgf8_status pgf8_fp8_linear_dynamic_noalloc(const void *x, pgf8_dtype xdt, int64
 }
 
 } // extern "C"
+
+// ------------------------------------------------------------------ block-scaled operators
+#include "block_api.cuh"
