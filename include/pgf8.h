@@ -709,6 +709,73 @@ size_t pgf8_fp8_block_linear_dynamic_workspace_size(int64_t M, int64_t K);
 size_t pgf8_fp8_block_linear_dynamic_scales_offset(int64_t M, int64_t K);
 
 /* ------------------------------------------------------------------------
+ * A mixture-of-experts layer for a few tokens (a decode batch), the experts'
+ * weights in E4M3 with 128 x 128 block scales ("C++ and FP8" §3.3: the FP8
+ * dataflow; the pages have no layer of this kind):
+ *   for each token t and chosen expert e with weight w[t,e]
+ *     g = xq[t] . W1[e]^T,  u = xq[t] . W3[e]^T     (binary32 sums)
+ *     h = g / (1 + exp(-g)) * u                     (binary32)
+ *     y[t] += w[t,e] * (hq . W2[e]^T)
+ * with xq and hq the E4M3 codes of x and h, one scale per 1 x 128 group (as
+ * pgf8_fp8_quantize_blocks), every product scaled block by block as in
+ * pgf8_fp8_block_linear, the sum over experts in binary32 in ascending order
+ * of e and one rounding to ydt.
+ *
+ * x       [tokens, hidden] f32, f16 or bf16, row stride ldx; tokens 0..64
+ *         (0: no-op), hidden and inter multiples of 16 in 16..2^20.
+ * w13     [experts, 2 * inter, hidden] codes: the gate matrix W1 above the up
+ *         matrix W3; s13 [experts, 2, ceil(inter/128), ceil(hidden/128)]: the
+ *         two matrices have blocks of their own (pgf8_fp8_quantize_blocks of
+ *         [2 * experts, inter, hidden]).
+ * w2      [experts, hidden, inter] codes, s2 [experts, ceil(hidden/128),
+ *         ceil(inter/128)].  experts 1..512.
+ * routing With logits [tokens, experts] (ldt f32, f16 or bf16, row stride
+ *         ldl): each token takes its top_k (1..16, <= experts) largest
+ *         logits, ties to the lower index; NaN and -inf are never chosen.  The
+ *         weights are the chosen experts' shares of the softmax over all
+ *         experts (PGF8_MOE_SOFTMAX) or their sigmoids (PGF8_MOE_SIGMOID), divided
+ *         by their sum when renormalise is set, times factor.  ids [tokens,
+ *         top_k] and weights [tokens, top_k] receive the choices, largest
+ *         logit first (-1 and 0 where too few can be chosen); either may be
+ *         NULL.
+ *         Without logits (NULL) ids and weights are read.  An id outside
+ *         [0, experts) leaves its slot out (padding, another rank's expert); an
+ *         expert that a token names twice counts with both weights.
+ * A token without any expert gets y = 0.
+ * Weights of experts that no token chose are not read.
+ * workspace: pgf8_fp8_moe_workspace_size(...) bytes (0 for sizes that the
+ * layer refuses), 16-byte aligned, not read before it is written (no
+ * zero-fill); one call at a time may use it.  x, w13, w2, y 16-byte aligned,
+ * y contiguous [tokens, hidden] and apart from every input.  Deterministic.
+ * Three launches; PGF8_FLAG_OVERLAP_PREVIOUS applies to the first, which reads
+ * nothing before the previous kernel has completed; the third may read w2 before
+ * the second has finished.
+ * ---------------------------------------------------------------------- */
+typedef enum { PGF8_MOE_SOFTMAX = 0, PGF8_MOE_SIGMOID = 1 } pgf8_moe_score;
+
+typedef struct {
+    const void *x;
+    const uint8_t *w13;
+    const float *s13;
+    const uint8_t *w2;
+    const float *s2;
+    const void *logits;      /* or NULL: ids and weights are given */
+    int32_t *ids;
+    float *weights;
+    void *y;
+    void *workspace;
+    size_t workspace_bytes;
+    int64_t tokens, hidden, inter, experts, top_k, ldx, ldl;
+    int32_t xdt, ldt, ydt;   /* pgf8_dtype of x, logits, y */
+    int32_t score;           /* pgf8_moe_score */
+    int32_t renormalise;
+    float factor;
+} pgf8_fp8_moe_layer;
+
+pgf8_status pgf8_fp8_moe(const pgf8_fp8_moe_layer *layer, int32_t flags, void *stream);
+size_t pgf8_fp8_moe_workspace_size(int64_t tokens, int64_t hidden, int64_t inter, int64_t experts, int64_t top_k);
+
+/* ------------------------------------------------------------------------
  * Allocation-free dynamic FP8 linear.  The pages have no counterpart of this
  * entry point; it exists for callers that cannot hand the library a
  * workspace: a host program that links only this C library and has no

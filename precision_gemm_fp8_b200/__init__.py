@@ -32,6 +32,7 @@ F32, F16, BF16 = 0, 1, 2
 SCALE_DYNAMIC, SCALE_STATIC = 0, 1
 NESTED_FP16, NESTED_FP8 = 0, 1
 PATH_AUTO, PATH_SKINNY, PATH_TILED, PATH_STREAMK, PATH_TILED_PAIR = 0, 1, 2, 3, 4
+MOE_SOFTMAX, MOE_SIGMOID = 0, 1
 FLAG_OVERLAP_PREVIOUS = 1
 FLAG_FUSED_QUANT = 2
 FLAG_ATTN_MMA = 4
@@ -59,6 +60,17 @@ class Fp8Layer(ctypes.Structure):
 class Fp8GemmLayer(ctypes.Structure):
     _fields_ = [("aq", ctypes.c_void_p), ("sa", ctypes.c_void_p), ("wq", ctypes.c_void_p), ("sw", ctypes.c_void_p),
                 ("y", ctypes.c_void_p), ("M", ctypes.c_int64), ("K", ctypes.c_int64), ("N", ctypes.c_int64)]
+
+
+class MoeLayer(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("w13", ctypes.c_void_p), ("s13", ctypes.c_void_p), ("w2", ctypes.c_void_p),
+                ("s2", ctypes.c_void_p), ("logits", ctypes.c_void_p), ("ids", ctypes.c_void_p),
+                ("weights", ctypes.c_void_p), ("y", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_size_t), ("tokens", ctypes.c_int64), ("hidden", ctypes.c_int64),
+                ("inter", ctypes.c_int64), ("experts", ctypes.c_int64), ("top_k", ctypes.c_int64),
+                ("ldx", ctypes.c_int64), ("ldl", ctypes.c_int64), ("xdt", ctypes.c_int32), ("ldt", ctypes.c_int32),
+                ("ydt", ctypes.c_int32), ("score", ctypes.c_int32), ("renormalise", ctypes.c_int32),
+                ("factor", ctypes.c_float)]
 
 
 class NestedLayer(ctypes.Structure):
@@ -118,6 +130,8 @@ _SIGS = {
                                       _i32),
     "pgf8_fp8_block_linear_dynamic_workspace_size": ([_i64, _i64], _sz),
     "pgf8_fp8_block_linear_dynamic_scales_offset": ([_i64, _i64], _sz),
+    "pgf8_fp8_moe": ([ctypes.POINTER(MoeLayer), _i32, _vp], _i32),
+    "pgf8_fp8_moe_workspace_size": ([_i64, _i64, _i64, _i64, _i64], _sz),
     "pgf8_last_cuda_error": ([ctypes.POINTER(ctypes.c_int)], _i32),
     "pgf8_device_status": ([_vp], _i32),
     "pgf8_selftest_bounded_wait": ([_i64, _vp], _i32),
@@ -949,6 +963,70 @@ def fp8_block_linear_dynamic(x: torch.Tensor, wq: torch.Tensor, sw: torch.Tensor
 def fp8_block_linear_dynamic_workspace_size(M: int, K: int) -> int:
     """Workspace bytes of fp8_block_linear_dynamic (no zero-fill needed)."""
     return int(lib.pgf8_fp8_block_linear_dynamic_workspace_size(M, K))
+
+
+def fp8_moe(x: torch.Tensor, w13: torch.Tensor, s13: torch.Tensor, w2: torch.Tensor, s2: torch.Tensor,
+            logits: torch.Tensor | None = None, top_k: int | None = None, score: int = MOE_SOFTMAX,
+            renormalise: bool = True, factor: float = 1.0, ids: torch.Tensor | None = None,
+            weights: torch.Tensor | None = None, y: torch.Tensor | None = None,
+            out_dtype: torch.dtype = torch.bfloat16, workspace: torch.Tensor | None = None, flags: int = 0,
+            stream=None):
+    """A mixture-of-experts layer on x [T, H] (T <= 64; f32, f16 or bf16; rows
+    may be strided): experts of E4M3 weights w13 [E, 2F, H] (gate above up) and
+    w2 [E, H, F] with block scales s13 [E, 2, ceil(F / 128), ceil(H / 128)] and
+    s2 [E, ceil(H / 128), ceil(F / 128)], as fp8_quantize_blocks(..., 128) gives
+    them for [E, 2, F, H] (viewed as [2E, F, H]) and [E, H, F].
+
+    Routing: from logits [T, E] and top_k (score MOE_SOFTMAX or MOE_SIGMOID,
+    renormalised over the choices or not, times factor), or from given ids
+    int32 [T, k] and weights f32 [T, k] (ids outside [0, E) are left out).
+    Returns (y [T, H], ids, weights)."""
+    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
+        raise ValueError("x must be [T, H] with contiguous rows")
+    T, H = x.shape
+    if w13.dim() != 3 or w13.shape[1] % 2:
+        raise ValueError("w13 must be [E, 2F, H]")
+    E, F = w13.shape[0], w13.shape[1] // 2
+    _want(w13, (E, 2 * F, H), torch.uint8, "w13")
+    _want(s13, (E, 2, _blocks(F), _blocks(H)), torch.float32, "s13")
+    _want(w2, (E, H, F), torch.uint8, "w2")
+    _want(s2, (E, _blocks(H), _blocks(F)), torch.float32, "s2")
+    if logits is not None:
+        if top_k is None:
+            raise ValueError("routing from logits needs top_k")
+        if tuple(logits.shape) != (T, E) or (E > 1 and logits.stride(1) != 1):
+            raise ValueError(f"logits must be [{T}, {E}] with contiguous rows")
+        lcode, ldl = _code(logits.dtype, "logits"), _lead(logits) if T else E
+    else:
+        if ids is None or weights is None:
+            raise ValueError("fp8_moe needs logits and top_k, or ids and weights")
+        top_k = ids.shape[-1] if top_k is None else top_k
+        lcode, ldl = F32, E
+    if ids is not None:
+        _want(ids, (T, top_k), torch.int32, "ids")
+    if weights is not None:
+        _want(weights, (T, top_k), torch.float32, "weights")
+    xcode = _code(x.dtype, "activation")
+    with _On(x.device, stream, w13, s13, w2, s2, logits, ids, weights, y, workspace) as handle:
+        y, ycode = _block_out(y, (T, H), out_dtype, x.device)
+        if ids is None:
+            ids = torch.empty((T, top_k), dtype=torch.int32, device=x.device)
+        if weights is None:
+            weights = torch.empty((T, top_k), dtype=torch.float32, device=x.device)
+        if workspace is None:
+            workspace = torch.empty(lib.pgf8_fp8_moe_workspace_size(T, H, F, E, top_k), dtype=torch.uint8,
+                                    device=x.device)
+        layer = MoeLayer(x.data_ptr(), w13.data_ptr(), s13.data_ptr(), w2.data_ptr(), s2.data_ptr(),
+                         None if logits is None else logits.data_ptr(), ids.data_ptr(), weights.data_ptr(),
+                         y.data_ptr(), workspace.data_ptr(), _nbytes(workspace), T, H, F, E, top_k,
+                         _lead(x) if T else H, ldl, xcode, lcode, ycode, score, 1 if renormalise else 0, factor)
+        _check(lib.pgf8_fp8_moe(ctypes.byref(layer), flags, handle), "fp8_moe")
+    return y, ids, weights
+
+
+def fp8_moe_workspace_size(tokens: int, hidden: int, inter: int, experts: int, top_k: int) -> int:
+    """Workspace bytes of fp8_moe (no zero-fill needed)."""
+    return int(lib.pgf8_fp8_moe_workspace_size(tokens, hidden, inter, experts, top_k))
 
 
 def selftest_row_division(divisors: torch.Tensor, stream=None):

@@ -19,7 +19,8 @@ LIB = os.path.join(PKG, "libpgf8.so")
 SOURCES = ["pgf8_api.cu"]
 DEPS = ["pgf8_api.cu", "gemm.cuh", "gemm_persistent.cuh", "gemm_streamk.cuh", "gemm_2sm.cuh", "gemm_group.cuh", "quantize.cuh", "sm100_ptx.cuh",
         "kvcache.cuh", "attention.cuh", "attention_context.cuh", "gemm_pair_group.cuh", "gemm_persistent_swap.cuh",
-        "block_api.cuh", "gemm_block.cuh", "quantize_blocks.cuh", "packed_ptx.cuh"]
+        "block_api.cuh", "gemm_block.cuh", "quantize_blocks.cuh", "packed_ptx.cuh",
+        "moe_api.cuh", "moe.cuh"]
 
 
 def _nvcc() -> str:

@@ -1,0 +1,853 @@
+// A mixture-of-experts layer for a few tokens (T <= 64), E4M3 weights with
+// 128 x 128 block scales, in three launches:
+//   moe_plan_kernel     routing (top-k of the logits) and the list of the chosen
+//                       experts' tokens by one CTA; the others quantise x per
+//                       1 x 128 group
+//   moe_gate_up_kernel  for every chosen expert and 128 hidden features:
+//                       g = xq W1, u = xq W3, h = silu(g) u in binary32, E4M3
+//                       codes of h with one scale per 1 x 128 group
+//   moe_down_kernel     y[t] = sum over the chosen experts of w[t, e] hq W2[e]
+//
+// A few tokens touch nearly as many experts as they choose, so the layer is
+// a stream of the chosen experts' weights (3 H F bytes each) and everything
+// else has to hide behind it.  Both products keep the weights as the 128-row
+// MMA operand and the tokens as the narrow one, accumulate one k-block at a
+// time in tensor memory and add it with its scales in registers, as
+// gemm_block.cuh does, and split their sums over a thread-block cluster,
+// joined in rank order (deterministic, no atomics on sums).
+//   gate+up: x's codes are the same for every expert, so the token operand is
+//     all T tokens whatever the expert's own tokens are: one contiguous tile
+//     instead of a gather; the MMA has time for the unused columns.
+//   down: an expert's tokens are consecutive rows of the hidden codes
+//     (sorted by expert, then token), only those are loaded; the experts'
+//     products run one after another through the same CTA, so the sum over
+//     experts is taken in shared memory in expert order and needs no
+//     combining launch.
+#pragma once
+
+#include "gemm_block.cuh"
+#include "quantize_blocks.cuh"
+
+namespace pgf8 {
+
+constexpr int kMoeMaxTokens = 64;     // one 64-bit mask of tokens per expert
+constexpr int kMoeMaxExperts = 512;   // 16 logits a lane
+constexpr int kMoeMaxTopK = 16;
+constexpr int kMoePlanThreads = 1024; // one thread per (token, choice) pair
+
+enum : int { kMoeSoftmax = 0, kMoeSigmoid = 1 };
+
+// What the plan kernel leaves for the other two.
+struct MoePlan {
+    int *active;      // [1] number of chosen experts
+    int4 *experts;    // [min(E, T k)] (expert, first row, rows, 0) in expert order
+    int *tok;         // [T k] token of each row of the hidden codes
+    float *weight;    // [T k] its weight
+};
+
+struct MoeRouteParams {
+    const void *x;         // [T, H], row stride ldx
+    int64_t ldx;
+    int T, H, hblocks;     // hblocks = ceil(H / 128)
+    uint8_t *xq;           // [T, H]
+    float *sx;             // [T, hblocks]
+    const void *logits;    // [T, E], row stride ldl; null: ids / weights are given
+    int64_t ldl;
+    int E, K;              // K choices a token
+    int score, renorm;
+    float factor;
+    int *ids;              // [T, K]; written with logits (may then be null), read without
+    float *weights;        // [T, K]
+    MoePlan plan;
+};
+
+__device__ __forceinline__ float to_float(float v) { return v; }
+__device__ __forceinline__ float to_float(__half v) { return __half2float(v); }
+__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+// One warp routes one token: the K largest logits (ties to the lowest index;
+// NaN and -inf are never chosen: id -1, weight 0), their softmax over all E or
+// their sigmoids, divided by their sum if asked, times factor.
+template <typename L>
+__device__ __forceinline__ void route_token(const MoeRouteParams &p, int t, int *sid, float *sw)
+{
+    constexpr int PER = kMoeMaxExperts / 32;
+    const int lane = threadIdx.x & 31;
+    const float ninf = -INFINITY;
+    const L *row = static_cast<const L *>(p.logits) + static_cast<int64_t>(t) * p.ldl;
+    float v[PER];
+    float top = ninf;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int e = lane + 32 * i;
+        float f = e < p.E ? to_float(row[e]) : ninf;
+        v[i] = f != f ? ninf : f;
+        top = fmaxf(top, v[i]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    float sum = 0.0f;
+    if (p.score == kMoeSoftmax && top > ninf) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            sum += v[i] > ninf ? expf(v[i] - top) : 0.0f;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    }
+    unsigned taken = 0;
+    float mine = 0.0f, chosen_sum = 0.0f;   // lane j keeps choice j
+    int my_id = -1;
+    for (int j = 0; j < p.K; ++j) {
+        float best = ninf;
+        int at = 0x7FFFFFFF;
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (!((taken >> i) & 1u) && v[i] > best) {
+                best = v[i];
+                at = lane + 32 * i;
+            }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            const float ob = __shfl_xor_sync(0xffffffffu, best, o);
+            const int oa = __shfl_xor_sync(0xffffffffu, at, o);
+            if (ob > best || (ob == best && oa < at)) {
+                best = ob;
+                at = oa;
+            }
+        }
+        if (best == ninf)
+            break;   // nothing left to choose (the same in every lane)
+        if ((at & 31) == lane)
+            taken |= 1u << (at >> 5);
+        const float w = p.score == kMoeSoftmax ? __fdiv_rn(expf(best - top), sum)
+                                               : __fdiv_rn(1.0f, 1.0f + expf(-best));
+        chosen_sum += w;
+        if (lane == j) {
+            mine = w;
+            my_id = at;
+        }
+    }
+    if (lane < p.K) {
+        if (p.renorm)
+            mine = chosen_sum != 0.0f ? __fdiv_rn(mine, chosen_sum) : 0.0f;
+        mine *= p.factor;
+        if (my_id < 0)
+            mine = 0.0f;
+        sid[t * p.K + lane] = my_id;
+        sw[t * p.K + lane] = mine;
+        if (p.ids)
+            p.ids[t * p.K + lane] = my_id;
+        if (p.weights)
+            p.weights[t * p.K + lane] = mine;
+    }
+}
+
+// Inclusive sum over the CTA's kMoePlanThreads threads (red: 32 ints).
+__device__ __forceinline__ int plan_scan(int v, int *red)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o)
+            v += u;
+    }
+    if (lane == 31)
+        red[warp] = v;
+    __syncthreads();
+    if (warp == 0) {
+        int w = red[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, w, o);
+            if (lane >= o)
+                w += u;
+        }
+        red[lane] = w;
+    }
+    __syncthreads();
+    const int r = v + (warp > 0 ? red[warp - 1] : 0);
+    __syncthreads();   // red may be written again
+    return r;
+}
+
+// Block 0 routes and plans; the others quantise x, 128 groups each.
+template <typename T, typename L>
+__global__ void __launch_bounds__(kMoePlanThreads) moe_plan_kernel(const MoeRouteParams p)
+{
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const int tid = threadIdx.x;
+    if (blockIdx.x > 0) {
+        const int g = (static_cast<int>(blockIdx.x) - 1) * (kMoePlanThreads / 8) + (tid >> 3);
+        const int row = g / p.hblocks, grp = g - row * p.hblocks;
+        const int c = grp * 128 + (tid & 7) * 16;
+        const bool live = row < p.T && c < p.H;
+        Vec16<T> v;
+        float a = 0.0f;
+        if (live) {
+            v.load(static_cast<const T *>(p.x) + static_cast<int64_t>(row) * p.ldx + c);
+            a = amax16(v.v);
+        }
+        a = group_max8(a);
+        if (!live)
+            return;
+        const float s = block_scale(a);
+        *reinterpret_cast<uint4 *>(p.xq + static_cast<int64_t>(row) * p.H + c) = encode16(v.v, RowDivisor(s));
+        if ((tid & 7) == 0)
+            p.sx[row * p.hblocks + grp] = s;
+        return;
+    }
+
+    __shared__ int sid[kMoeMaxTokens * kMoeMaxTopK];
+    __shared__ float sw[kMoeMaxTokens * kMoeMaxTopK];
+    __shared__ unsigned mask[kMoeMaxExperts][2];   // tokens of each expert
+    __shared__ int first[kMoeMaxExperts];          // its first row
+    __shared__ int red[32];
+    const int pairs = p.T * p.K;
+    if (tid < kMoeMaxExperts)
+        mask[tid][0] = mask[tid][1] = 0u;
+    if (p.logits) {
+        for (int t = tid >> 5; t < p.T; t += kMoePlanThreads / 32)
+            route_token<L>(p, t, sid, sw);
+    } else if (tid < pairs) {
+        sid[tid] = p.ids[tid];
+        sw[tid] = p.weights[tid];
+    }
+    __syncthreads();
+    const int t = tid / p.K;
+    const int e = tid < pairs ? sid[tid] : -1;
+    const bool chosen = e >= 0 && e < p.E;
+    if (chosen)
+        atomicOr(&mask[e][t >> 5], 1u << (t & 31));
+    __syncthreads();
+    const int rows = tid < p.E ? __popc(mask[tid][0]) + __popc(mask[tid][1]) : 0;
+    // both sums in one scan: rows (at most 1024) above the count of experts (at most 512)
+    const int both = plan_scan((rows << 16) | (rows > 0 ? 1 : 0), red);
+    if (tid < p.E) {
+        const int row0 = (both >> 16) - rows;
+        first[tid] = row0;
+        if (rows > 0)
+            p.plan.experts[(both & 0xFFFF) - 1] = make_int4(tid, row0, rows, 0);
+    }
+    if (tid == kMoePlanThreads - 1)
+        *p.plan.active = both & 0xFFFF;
+    __syncthreads();
+    if (chosen) {
+        // a token that names an expert twice is one row with both weights
+        const int j0 = t * p.K;
+        float w = 0.0f;
+        bool again = false;
+        for (int j = j0; j < j0 + p.K; ++j)
+            if (sid[j] == e) {
+                again = again || j < tid;
+                w += sw[j];
+            }
+        if (!again) {
+            const unsigned lo = t < 32 ? (1u << t) - 1u : 0xFFFFFFFFu;
+            const unsigned hi = t < 32 ? 0u : (1u << (t - 32)) - 1u;
+            const int row = first[e] + __popc(mask[e][0] & lo) + __popc(mask[e][1] & hi);
+            p.plan.tok[row] = t;
+            p.plan.weight[row] = w;
+        }
+    }
+}
+
+// ------------------------------------------------------------------ gate + up
+template <int BN_, int STAGES_, int NBUF_> struct MoeUpCfg {
+    static constexpr int BN = BN_;
+    static constexpr int STAGES = STAGES_;
+    static constexpr int NBUF = NBUF_;                 // buffers of 2 BN columns (gate, up)
+    static constexpr int kThreads = 192;
+    static constexpr int kTileA = 128 * 128;
+    static constexpr int kStage = 2 * kTileA + BN * 128;
+    static constexpr int kTmemCols = NBUF * 2 * BN;
+    static constexpr int kRingBytes = STAGES * kStage; // reused for the partial tiles [2][BN][128] f32
+    static constexpr int kChunk = BN == 16 ? 8 : 4;    // k-blocks of scales staged at a time
+    static constexpr int kScalePitch = BN + 4;
+    static constexpr int kScaleOffset = kRingBytes;
+    static constexpr int kScaleBytes = 2 * 2 * kChunk * kScalePitch * 4;
+    static constexpr int kCtlOffset = kScaleOffset + kScaleBytes;
+    static constexpr int kSmemBytes = kCtlOffset + 512 + 1024;
+    static_assert(BN == 16 || BN == 32 || BN == 64, "token tile");
+    static_assert(STAGES <= 8 && NBUF <= 8, "barriers");
+    static_assert((kTmemCols & (kTmemCols - 1)) == 0 && kTmemCols >= 32 && kTmemCols <= 256, "tensor memory");
+    static_assert(kRingBytes >= 2 * BN * 128 * 4, "partial tiles");
+    static_assert(2 * (kSmemBytes + 1024) <= 228 * 1024, "two CTAs per SM");
+};
+
+struct MoeUpParams {
+    int T, F, hblocks, fblocks;
+    const float *sx;     // [T, hblocks]
+    const float *s13;    // [E, 2, fblocks, hblocks]
+    uint8_t *hq;         // [T k, F]
+    float *sh;           // [T k, fblocks]
+    MoePlan plan;
+};
+
+// Grid (fblocks, min(E, T k), splits): cluster of `splits` CTAs along z for
+// 128 hidden features of one chosen expert, each a range of k-blocks of H.
+template <class C>
+__global__ void __launch_bounds__(C::kThreads)
+    moe_gate_up_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
+                       const MoeUpParams p)
+{
+    constexpr int BN = C::BN, STAGES = C::STAGES, NBUF = C::NBUF;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    float *sc = reinterpret_cast<float *>(smem + C::kScaleOffset);
+    BlockCtl *ctl = reinterpret_cast<BlockCtl *>(smem + C::kCtlOffset);
+    volatile int *abort_flag = &ctl->abort;
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const int f0 = static_cast<int>(blockIdx.x) * 128;
+    const int splits = static_cast<int>(gridDim.z);
+    const int kb0 = static_cast<int>(static_cast<int64_t>(p.hblocks) * blockIdx.z / splits);
+    const int kb1 = static_cast<int>(static_cast<int64_t>(p.hblocks) * (blockIdx.z + 1) / splits);
+
+    // The plan comes from the kernel before.  Dependents (the down kernel) may
+    // start once every CTA of this grid is past its wait: the plan is complete
+    // then, and they read it, and weights, before this grid has finished.
+    grid_dependency_wait();
+    grid_launch_dependents();
+    if (static_cast<int>(blockIdx.y) >= __ldcg(p.plan.active))
+        return;   // the whole cluster
+    const int4 ex = __ldcg(p.plan.experts + blockIdx.y);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&ctl->full[s], 1);
+            mbar_init(&ctl->empty[s], 1);
+        }
+        for (int b = 0; b < NBUF; ++b) {
+            mbar_init(&ctl->acc_full[b], 1);
+            mbar_init(&ctl->acc_empty[b], 4);
+        }
+        mbar_init(&ctl->drain, 1);
+        ctl->abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(&ctl->tmem_base, C::kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = ctl->tmem_base;
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ producer
+        if (lane == 0) {
+            const uint64_t pol_w = policy_evict_first();
+            const uint64_t pol_x = policy_evict_last();
+            const int row = ex.x * 2 * p.F + f0;
+            int s = 0, issued = 0;
+            uint32_t ph = 1;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!wait_bounded(&ctl->empty[s], ph, abort_flag))
+                    break;
+                uint8_t *st = smem + s * C::kStage;
+                mbar_arrive_expect_tx(&ctl->full[s], C::kStage);
+                tma_load_2d_hint(st, &tmW, &ctl->full[s], kb * 128, row, pol_w);
+                tma_load_2d_hint(st + C::kTileA, &tmW, &ctl->full[s], kb * 128, row + p.F, pol_w);
+                tma_load_2d_hint(st + 2 * C::kTileA, &tmX, &ctl->full[s], kb * 128, 0, pol_x);
+                ++issued;
+                if (++s == STAGES) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            }
+            if (*abort_flag) {
+                for (int j = 0; j < STAGES && j < issued; ++j)
+                    wait_drain(&ctl->full[j], static_cast<uint32_t>((issued - 1 - j) / STAGES) & 1u);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer
+        if (lane == 0) {
+            constexpr uint32_t idesc = make_idesc(128, BN, 0, 0);
+            int s = 0, b = 0;
+            uint32_t ph = 0, bph = 1;
+            bool ok = true;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!wait_bounded(&ctl->acc_empty[b], bph, abort_flag) ||
+                    !wait_bounded(&ctl->full[s], ph, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t a_addr = smem_u32(smem + s * C::kStage);
+                const uint32_t x_addr = a_addr + 2 * C::kTileA;
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        umma_f8f6f4(tmem + (b * 2 + half) * BN, sdesc_sw128(a_addr + half * C::kTileA + k * 32),
+                                    sdesc_sw128(x_addr + k * 32), idesc, k > 0 ? 1u : 0u);
+                umma_commit(&ctl->empty[s]);
+                umma_commit(&ctl->acc_full[b]);
+                if (++s == STAGES) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+                if (++b == NBUF) {
+                    b = 0;
+                    bph ^= 1u;
+                }
+            }
+            if (!ok) {
+                umma_commit(&ctl->drain);
+                wait_drain(&ctl->drain, 0);
+            }
+        }
+        __syncwarp();
+    }
+
+    uint64_t accg[BN / 2], accu[BN / 2];
+    const int qd = warp & 3;
+    const int r = qd * 32 + lane;
+    if (warp >= 2) {
+        // ------------------------------------------------------------ scales and accumulation
+#pragma unroll
+        for (int j = 0; j < BN / 2; ++j)
+            accg[j] = accu[j] = 0;
+        const uint32_t t_row = tmem + (static_cast<uint32_t>(qd * 32) << 16);
+        const int et = static_cast<int>(threadIdx.x) - 64;
+        constexpr int CH = C::kChunk, PER = BN * CH / 128;
+        float pre[PER], wg, wu;
+        const float *swg = p.s13 + (static_cast<int64_t>(ex.x) * 2 * p.fblocks + blockIdx.x) * p.hblocks;
+        const float *swu = swg + static_cast<int64_t>(p.fblocks) * p.hblocks;
+        auto fetch = [&](int kb) {
+            const int k = kb + (et & (CH - 1));
+            wg = k < kb1 ? __ldg(swg + k) : 0.0f;
+            wu = k < kb1 ? __ldg(swu + k) : 0.0f;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const int t = (et + 128 * i) / CH;
+                pre[i] = (k < kb1 && t < p.T) ? __ldcg(p.sx + t * p.hblocks + k) : 0.0f;
+            }
+        };
+        fetch(kb0);
+        int b = 0;
+        uint32_t bph = 0;
+        bool ok = true;
+        for (int i = 0; i < kb1 - kb0; ++i) {
+            float *bufg = sc + ((i / CH) & 1) * 2 * CH * C::kScalePitch;
+            float *bufu = bufg + CH * C::kScalePitch;
+            if (i % CH == 0) {
+#pragma unroll
+                for (int j = 0; j < PER; ++j) {
+                    const int at = (et & (CH - 1)) * C::kScalePitch + ((et + 128 * j) / CH);
+                    bufg[at] = pre[j] * wg;
+                    bufu[at] = pre[j] * wu;
+                }
+                fetch(kb0 + i + CH);
+                bar_sync_warps2to5();
+            }
+            ok = ok && wait_bounded(&ctl->acc_full[b], bph, abort_flag);
+            ok = __all_sync(0xffffffffu, ok);
+            if (ok) {
+                tc_fence_after();
+                const int at = (i % CH) * C::kScalePitch;
+                add_scaled<BN>(t_row + b * 2 * BN, bufg + at, accg);
+                add_scaled<BN>(t_row + b * 2 * BN + BN, bufu + at, accu);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&ctl->acc_empty[b]);
+            }
+            if (++b == NBUF) {
+                b = 0;
+                bph ^= 1u;
+            }
+        }
+    }
+    __syncwarp();
+
+    // ---------------------------------------------------------------- partial tiles, gate, codes
+    float *part = reinterpret_cast<float *>(smem);
+    tc_fence_before();
+    __syncthreads();   // the ring is idle
+    if (warp >= 2) {
+#pragma unroll
+        for (int c = 0; c < BN; c += 2) {
+            const float2 g = unpack_f32x2(accg[c / 2]), u = unpack_f32x2(accu[c / 2]);
+            part[c * 128 + r] = g.x;
+            part[(c + 1) * 128 + r] = g.y;
+            part[(BN + c) * 128 + r] = u.x;
+            part[(BN + c + 1) * 128 + r] = u.y;
+        }
+    }
+    if (splits > 1)
+        cluster_sync_all();
+    else
+        __syncthreads();
+    if (warp >= 2) {
+        // one warp to a row of hidden codes, four features a lane
+        const uint32_t base = smem_u32(part) + lane * 16;
+        const int f = f0 + lane * 4;
+        for (int i = static_cast<int>(blockIdx.z) + splits * (warp - 2); i < ex.z; i += 4 * splits) {
+            const int row = ex.y + i;
+            const uint32_t off = base + __ldcg(p.plan.tok + row) * 512;
+            float4 tg[8], tu[8];
+#pragma unroll
+            for (int z = 0; z < 8; ++z)
+                if (z < splits) {
+                    const uint32_t a = splits > 1 ? map_shared_rank(off, static_cast<uint32_t>(z)) : off;
+                    tg[z] = ld_shared_cluster_v4_relaxed(a);
+                    tu[z] = ld_shared_cluster_v4_relaxed(a + BN * 512);
+                }
+            float4 g = tg[0], u = tu[0];
+#pragma unroll
+            for (int z = 1; z < 8; ++z)
+                if (z < splits) {
+                    g = make_float4(g.x + tg[z].x, g.y + tg[z].y, g.z + tg[z].z, g.w + tg[z].w);
+                    u = make_float4(u.x + tu[z].x, u.y + tu[z].y, u.z + tu[z].z, u.w + tu[z].w);
+                }
+            const bool live = f < p.F;   // F % 16 == 0: a lane's four features exist together
+            float h[4] = {silu_mul(g.x, u.x), silu_mul(g.y, u.y), silu_mul(g.z, u.z), silu_mul(g.w, u.w)};
+            float a = 0.0f;
+            if (live)
+                a = fmaxf(fmaxf(fabsf(h[0]), fabsf(h[1])), fmaxf(fabsf(h[2]), fabsf(h[3])));
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+                a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+            const float s = block_scale(a);
+            if (live)
+                *reinterpret_cast<uint32_t *>(p.hq + static_cast<int64_t>(row) * p.F + f) =
+                    static_cast<uint32_t>(cvt_e4m3x2(__fdiv_rn(h[0], s), __fdiv_rn(h[1], s))) |
+                    (static_cast<uint32_t>(cvt_e4m3x2(__fdiv_rn(h[2], s), __fdiv_rn(h[3], s))) << 16);
+            if (lane == 0)
+                p.sh[row * p.fblocks + blockIdx.x] = s;
+        }
+    }
+    if (splits > 1)
+        cluster_sync_all();   // no CTA leaves while its partial may still be read
+    else
+        __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::kTmemCols);
+    }
+}
+
+// ------------------------------------------------------------------ down
+template <int BN_, int STAGES_, int NBUF_> struct MoeDownCfg {
+    static constexpr int BN = BN_;
+    static constexpr int STAGES = STAGES_;
+    static constexpr int NBUF = NBUF_;
+    static constexpr int kThreads = 192;
+    static constexpr int kTileA = 128 * 128;
+    static constexpr int kStage = kTileA + BN * 128;
+    static constexpr int kTmemCols = NBUF * BN < 32 ? 32 : NBUF * BN;
+    static constexpr int kRingBytes = STAGES * kStage;
+    static constexpr int kSumOffset = kRingBytes;        // [BN][128] f32: the output tile, by token
+    static constexpr int kScalePitch = BN + 4;
+    static constexpr int kScaleOffset = kSumOffset + BN * 512;
+    static constexpr int kScaleBytes = 2 * kScaleChunk * kScalePitch * 4;
+    static constexpr int kCtlOffset = kScaleOffset + kScaleBytes;
+    static constexpr int kPlanOffset = kCtlOffset + 512; // experts (int4), tokens, weights: sized at launch
+    static constexpr int kSmemBytes = kPlanOffset + 1024;
+    static_assert(BN == 16 || BN == 32 || BN == 64, "token tile");
+    static_assert(STAGES <= 8 && NBUF <= 8, "barriers");
+    static_assert((kTmemCols & (kTmemCols - 1)) == 0 && kTmemCols <= 256, "tensor memory");
+};
+
+struct MoeDownParams {
+    int T, H, fblocks;
+    int max_active, pairs;   // sizes of the plan's lists
+    const float *sh;         // [T k, fblocks]
+    const float *s2;         // [E, ceil(H / 128), fblocks]
+    void *y;                 // [T, H]
+    int ydt;
+    MoePlan plan;
+};
+
+// Grid (ceil(H / 128), 1, splits): a cluster of `splits` CTAs along z for 128
+// output features; the (expert, k-block of F) units of all chosen experts, in
+// that order, are dealt to its CTAs in equal contiguous ranges.
+template <class C>
+__global__ void __launch_bounds__(C::kThreads)
+    moe_down_kernel(const __grid_constant__ CUtensorMap tmH, const __grid_constant__ CUtensorMap tmW,
+                    const MoeDownParams p)
+{
+    constexpr int BN = C::BN, STAGES = C::STAGES, NBUF = C::NBUF;
+    grid_launch_dependents();
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    float *sum = reinterpret_cast<float *>(smem + C::kSumOffset);
+    float *sc = reinterpret_cast<float *>(smem + C::kScaleOffset);
+    BlockCtl *ctl = reinterpret_cast<BlockCtl *>(smem + C::kCtlOffset);
+    int4 *experts = reinterpret_cast<int4 *>(smem + C::kPlanOffset);
+    int *tok = reinterpret_cast<int *>(experts + p.max_active);
+    float *weight = reinterpret_cast<float *>(tok + p.pairs);
+    volatile int *abort_flag = &ctl->abort;
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const int splits = static_cast<int>(gridDim.z);
+
+    // The plan was complete before this grid could start (the gate+up kernel
+    // lets it start only after its own wait for the plan).
+    const int active = __ldcg(p.plan.active);
+    for (int i = threadIdx.x; i < active; i += C::kThreads)
+        experts[i] = __ldcg(p.plan.experts + i);
+    for (int i = threadIdx.x; i < p.pairs; i += C::kThreads) {
+        tok[i] = __ldcg(p.plan.tok + i);   // entries behind the last row are not used
+        weight[i] = __ldcg(p.plan.weight + i);
+    }
+    const int units = active * p.fblocks;
+    const int u0 = static_cast<int>(static_cast<int64_t>(units) * blockIdx.z / splits);
+    const int u1 = static_cast<int>(static_cast<int64_t>(units) * (blockIdx.z + 1) / splits);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&ctl->full[s], 1);
+            mbar_init(&ctl->empty[s], 1);
+        }
+        for (int b = 0; b < NBUF; ++b) {
+            mbar_init(&ctl->acc_full[b], 1);
+            mbar_init(&ctl->acc_empty[b], 4);
+        }
+        mbar_init(&ctl->drain, 1);
+        ctl->abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(&ctl->tmem_base, C::kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = ctl->tmem_base;
+    auto tokens16 = [](int rows) { return (rows + 15) & ~15; };   // the MMA's N
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ producer
+        if (lane == 0) {
+            const uint64_t pol_w = policy_evict_first();
+            const uint64_t pol_h = policy_evict_last();
+            auto load_w = [&](int s, int a, int kb) {
+                mbar_arrive_expect_tx(&ctl->full[s],
+                                      static_cast<uint32_t>(C::kTileA + tokens16(experts[a].z) * 128));
+                tma_load_2d_hint(smem + s * C::kStage, &tmW, &ctl->full[s], kb * 128,
+                                 experts[a].x * p.H + static_cast<int>(blockIdx.x) * 128, pol_w);
+            };
+            auto load_h = [&](int s, int a, int kb) {
+                for (int c = 0; c < experts[a].z; c += 16)
+                    tma_load_2d_hint(smem + s * C::kStage + C::kTileA + c * 128, &tmH, &ctl->full[s], kb * 128,
+                                     experts[a].y + c, pol_h);
+            };
+            // the first ring pass: weights at once, hidden codes when the gate+up kernel has finished
+            const int first = u1 - u0 < STAGES ? u1 - u0 : STAGES;
+            for (int i = 0; i < first; ++i)
+                load_w(i, (u0 + i) / p.fblocks, (u0 + i) % p.fblocks);
+            grid_dependency_wait();
+            for (int i = 0; i < first; ++i)
+                load_h(i, (u0 + i) / p.fblocks, (u0 + i) % p.fblocks);
+            int s = 0, issued = first;
+            uint32_t ph = 0;
+            int a = (u0 + first) / p.fblocks, kb = (u0 + first) % p.fblocks;
+            for (int u = u0 + first; u < u1; ++u) {
+                if (!wait_bounded(&ctl->empty[s], ph, abort_flag))
+                    break;
+                load_w(s, a, kb);
+                load_h(s, a, kb);
+                ++issued;
+                if (++kb == p.fblocks) {
+                    kb = 0;
+                    ++a;
+                }
+                if (++s == STAGES) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            }
+            if (*abort_flag) {
+                for (int j = 0; j < STAGES && j < issued; ++j)
+                    wait_drain(&ctl->full[j], static_cast<uint32_t>((issued - 1 - j) / STAGES) & 1u);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer
+        grid_dependency_wait();
+        if (lane == 0) {
+            int s = 0, b = 0;
+            uint32_t ph = 0, bph = 1;
+            bool ok = true;
+            int a = u0 / p.fblocks, kb = u0 % p.fblocks;
+            for (int u = u0; u < u1; ++u) {
+                if (!wait_bounded(&ctl->acc_empty[b], bph, abort_flag) ||
+                    !wait_bounded(&ctl->full[s], ph, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t idesc = make_idesc(128, tokens16(experts[a].z), 0, 0);
+                const uint32_t a_addr = smem_u32(smem + s * C::kStage);
+                const uint32_t h_addr = a_addr + C::kTileA;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    umma_f8f6f4(tmem + b * BN, sdesc_sw128(a_addr + k * 32), sdesc_sw128(h_addr + k * 32), idesc,
+                                k > 0 ? 1u : 0u);
+                umma_commit(&ctl->empty[s]);
+                umma_commit(&ctl->acc_full[b]);
+                if (++kb == p.fblocks) {
+                    kb = 0;
+                    ++a;
+                }
+                if (++s == STAGES) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+                if (++b == NBUF) {
+                    b = 0;
+                    bph ^= 1u;
+                }
+            }
+            if (!ok) {
+                umma_commit(&ctl->drain);
+                wait_drain(&ctl->drain, 0);
+            }
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------ scales, accumulation, sum over experts
+        const int qd = warp & 3;
+        const int r = qd * 32 + lane;   // this thread alone touches column r of `sum`
+        for (int c = 0; c < BN; ++c)
+            sum[c * 128 + r] = 0.0f;
+        float acc[BN];
+#pragma unroll
+        for (int j = 0; j < BN; ++j)
+            acc[j] = 0.0f;
+        grid_dependency_wait();         // the scales of the hidden codes
+        const uint32_t t_row = tmem + (static_cast<uint32_t>(qd * 32) << 16);
+        const int et = static_cast<int>(threadIdx.x) - 64;
+        constexpr int PER = BN * kScaleChunk / 128;
+        float pre[PER];
+        // sh[row, kb] * s2[e, feature block, kb] of 8 units from u: thread et's
+        // values are the expert's rows (et + 128 i) / 8 at unit u + et % 8
+        auto fetch = [&](int u) {
+            u += et & 7;
+            const bool in = u < u1;
+            const int a = in ? u / p.fblocks : 0;
+            const int k = in ? u - a * p.fblocks : 0;
+            const int4 ex = in ? experts[a] : make_int4(0, 0, 0, 0);
+            const float w =
+                in ? __ldg(p.s2 + (static_cast<int64_t>(ex.x) * gridDim.x + blockIdx.x) * p.fblocks + k) : 0.0f;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const int c = (et + 128 * i) >> 3;
+                pre[i] = c < ex.z ? __ldcg(p.sh + (ex.y + c) * p.fblocks + k) * w : 0.0f;
+            }
+        };
+        fetch(u0);
+        int b = 0;
+        uint32_t bph = 0;
+        bool ok = true;
+        int a = u0 / p.fblocks, kb = u0 % p.fblocks;
+        for (int i = 0; i < u1 - u0; ++i) {
+            float *buf = sc + ((i / kScaleChunk) & 1) * kScaleChunk * C::kScalePitch;
+            if (i % kScaleChunk == 0) {
+#pragma unroll
+                for (int j = 0; j < PER; ++j)
+                    buf[(et & 7) * C::kScalePitch + ((et + 128 * j) >> 3)] = pre[j];
+                fetch(u0 + i + kScaleChunk);
+                bar_sync_warps2to5();
+            }
+            ok = ok && wait_bounded(&ctl->acc_full[b], bph, abort_flag);
+            ok = __all_sync(0xffffffffu, ok);
+            const int rows = experts[a].z;
+            if (ok) {
+                tc_fence_after();
+                const float *s = buf + (i % kScaleChunk) * C::kScalePitch;
+#pragma unroll
+                for (int c0 = 0; c0 < BN; c0 += 16) {
+                    if (c0 < rows) {
+                        uint32_t v[16];
+                        tmem_ld_32x32b_x16(t_row + b * BN + c0, v);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int j = 0; j < 16; j += 4) {
+                            const float4 t = *reinterpret_cast<const float4 *>(s + c0 + j);
+                            acc[c0 + j] = fmaf(__uint_as_float(v[j]), t.x, acc[c0 + j]);
+                            acc[c0 + j + 1] = fmaf(__uint_as_float(v[j + 1]), t.y, acc[c0 + j + 1]);
+                            acc[c0 + j + 2] = fmaf(__uint_as_float(v[j + 2]), t.z, acc[c0 + j + 2]);
+                            acc[c0 + j + 3] = fmaf(__uint_as_float(v[j + 3]), t.w, acc[c0 + j + 3]);
+                        }
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&ctl->acc_empty[b]);
+            }
+            if (kb + 1 == p.fblocks || i + 1 == u1 - u0) {
+                // the expert's (or the range's) last unit: to the output tile, by token
+                const int row0 = experts[a].y;
+#pragma unroll
+                for (int c = 0; c < BN; ++c) {
+                    if (c < rows) {
+                        float *o = sum + tok[row0 + c] * 128 + r;
+                        *o = fmaf(acc[c], weight[row0 + c], *o);
+                    }
+                    acc[c] = 0.0f;
+                }
+            }
+            if (++kb == p.fblocks) {
+                kb = 0;
+                ++a;
+            }
+            if (++b == NBUF) {
+                b = 0;
+                bph ^= 1u;
+            }
+        }
+    }
+    __syncwarp();
+
+    // ---------------------------------------------------------------- output
+    tc_fence_before();
+    if (splits > 1)
+        cluster_sync_all();
+    else
+        __syncthreads();
+    if (warp >= 2) {
+        const int n4 = static_cast<int>(blockIdx.x) * 128 + lane * 4;
+        const uint32_t base = smem_u32(sum) + lane * 16;
+        for (int t = static_cast<int>(blockIdx.z) + splits * (warp - 2); n4 < p.H && t < p.T; t += 4 * splits) {
+            float4 q[8];
+#pragma unroll
+            for (int z = 0; z < 8; ++z)
+                if (z < splits) {
+                    const uint32_t off = base + t * 512;
+                    q[z] = ld_shared_cluster_v4_relaxed(
+                        splits > 1 ? map_shared_rank(off, static_cast<uint32_t>(z)) : off);
+                }
+            float4 v = q[0];
+#pragma unroll
+            for (int z = 1; z < 8; ++z)
+                if (z < splits)
+                    v = make_float4(v.x + q[z].x, v.y + q[z].y, v.z + q[z].z, v.w + q[z].w);
+            store_out4(p.y, static_cast<int64_t>(t) * p.H + n4, v, p.ydt);
+        }
+    }
+    if (splits > 1)
+        cluster_sync_all();   // no CTA leaves while its sums may still be read
+    else
+        __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::kTmemCols);
+    }
+}
+
+} // namespace pgf8

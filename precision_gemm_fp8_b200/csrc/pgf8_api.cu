@@ -2584,3 +2584,4 @@ pgf8_status pgf8_fp8_linear_dynamic_noalloc(const void *x, pgf8_dtype xdt, int64
 
 // ------------------------------------------------------------------ block-scaled operators
 #include "block_api.cuh"
+#include "moe_api.cuh"
