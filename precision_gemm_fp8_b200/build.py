@@ -20,7 +20,7 @@ SOURCES = ["pgf8_api.cu"]
 DEPS = ["pgf8_api.cu", "gemm.cuh", "gemm_persistent.cuh", "gemm_streamk.cuh", "gemm_2sm.cuh", "gemm_group.cuh", "quantize.cuh", "sm100_ptx.cuh",
         "kvcache.cuh", "attention.cuh", "attention_context.cuh", "gemm_pair_group.cuh", "gemm_persistent_swap.cuh",
         "block_api.cuh", "gemm_block.cuh", "quantize_blocks.cuh", "packed_ptx.cuh",
-        "moe_api.cuh", "moe.cuh"]
+        "moe_api.cuh", "moe.cuh", "gemm_block_pair.cuh"]
 
 
 def _nvcc() -> str:

@@ -4,6 +4,7 @@
 #pragma once
 
 #include "gemm_block.cuh"
+#include "gemm_block_pair.cuh"
 #include "quantize_blocks.cuh"
 
 namespace pgf8 {
@@ -91,6 +92,29 @@ static int block_splits(int64_t tiles, int64_t kblocks, int64_t slots)
     return 1;
 }
 
+static BlockParams block_params(const BlockLaunch &L)
+{
+    BlockParams p;
+    p.M = static_cast<int>(L.M);
+    p.N = static_cast<int>(L.N);
+    p.K = static_cast<int>(L.K);
+    p.kblocks = static_cast<int>(ceil_div(L.K, 128));
+    p.prefetch_w = L.prefetch_w;
+    p.sa = L.sa;
+    p.sw = L.sw;
+    p.y = L.y;
+    p.ydt = L.ydt;
+    return p;
+}
+
+template <class C> static bool block_maps(const BlockLaunch &L, CUtensorMap &tmX, CUtensorMap &tmW)
+{
+    return make_map(&tmX, L.aq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, L.M, L.K, 128, C::kRowsX,
+                    CU_TENSOR_MAP_SWIZZLE_128B) &&
+           make_map(&tmW, L.wq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, L.N, L.K, 128, C::kRowsW,
+                    CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
 template <class C> static pgf8_status launch_block(const BlockLaunch &L, int ctas_per_sm)
 {
     static PerDeviceSetup setup;
@@ -105,19 +129,9 @@ template <class C> static pgf8_status launch_block(const BlockLaunch &L, int cta
     if (attr_err != cudaSuccess)
         return cuda_fail(attr_err);
     CUtensorMap tmX, tmW;
-    if (!make_map(&tmX, L.aq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, L.M, L.K, 128, C::BN, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !make_map(&tmW, L.wq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, L.N, L.K, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B))
+    if (!block_maps<C>(L, tmX, tmW))
         return PGF8_ERR_UNSUPPORTED;
-    BlockParams p;
-    p.M = static_cast<int>(L.M);
-    p.N = static_cast<int>(L.N);
-    p.K = static_cast<int>(L.K);
-    p.kblocks = static_cast<int>(ceil_div(L.K, 128));
-    p.prefetch_w = L.prefetch_w;
-    p.sa = L.sa;
-    p.sw = L.sw;
-    p.y = L.y;
-    p.ydt = L.ydt;
+    const BlockParams p = block_params(L);
     const int64_t nt = ceil_div(L.N, 128), mt = ceil_div(L.M, C::BN);
     if (mt > 65535)
         return PGF8_ERR_UNSUPPORTED;   // the grid's y extent
@@ -134,6 +148,48 @@ template <class C> static pgf8_status launch_block(const BlockLaunch &L, int cta
     return e == cudaSuccess ? PGF8_OK : cuda_fail(e);
 }
 
+// SM pairs: clusters of two CTAs, as many as the GPU holds at once.
+template <class C> static pgf8_status launch_block_pair(const BlockLaunch &L)
+{
+    static PerDeviceSetup setup;
+    int pairs_fit = 1;
+    const cudaError_t err = setup_once_per_device(setup, [](int, int *v) {
+        cudaError_t e = cudaFuncSetAttribute(gemm_block_pair_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             C::kSmemBytes);
+        if (e != cudaSuccess)
+            return e;
+        cudaLaunchConfig_t q;
+        std::memset(&q, 0, sizeof(q));
+        q.gridDim = dim3(2 * num_sms(), 1, 1);
+        q.blockDim = dim3(C::kThreads, 1, 1);
+        q.dynamicSmemBytes = C::kSmemBytes;
+        cudaLaunchAttribute qa[2];
+        fill_attrs(q, qa, 1, 0, 2);
+        int n = 0;
+        e = cudaOccupancyMaxActiveClusters(&n, gemm_block_pair_kernel<C>, &q);
+        *v = n > 0 ? n : 1;
+        return e;
+    }, &pairs_fit);
+    if (err != cudaSuccess)
+        return cuda_fail(err);
+    CUtensorMap tmX, tmW;
+    if (!block_maps<C>(L, tmX, tmW))
+        return PGF8_ERR_UNSUPPORTED;
+    const int64_t tiles = ceil_div(L.M, 256) * ceil_div(L.N, C::BN);
+    if (tiles > 2147483647)
+        return PGF8_ERR_UNSUPPORTED;
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * (tiles < pairs_fit ? tiles : pairs_fit)), 1, 1);
+    cfg.blockDim = dim3(C::kThreads, 1, 1);
+    cfg.dynamicSmemBytes = C::kSmemBytes;
+    cfg.stream = L.stream;
+    cudaLaunchAttribute attrs[2];
+    fill_attrs(cfg, attrs, 1, 1, 2);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, gemm_block_pair_kernel<C>, tmX, tmW, block_params(L));
+    return e == cudaSuccess ? PGF8_OK : cuda_fail(e);
+}
+
 static pgf8_status block_linear_launch(const BlockLaunch &L)
 {
     if (L.M <= 16)
@@ -142,7 +198,17 @@ static pgf8_status block_linear_launch(const BlockLaunch &L)
         return launch_block<BlockCfg<32, 5, 4>>(L, 2);
     if (L.M <= 64)
         return launch_block<BlockCfg<64, 4, 4>>(L, 2);
-    return launch_block<BlockCfg<128, 6, 4>>(L, 1);
+    if (L.M <= 128)
+        return launch_block<BlockCfg<128, 6, 4>>(L, 1);
+    // 256-wide tiles unless half-width ones fill the rounds of pairs better: a
+    // round of those takes about 0.72 of the time (4096 x 8192 x 10240: 18
+    // rounds in 478 us against 9 in 340; 512 x 4096 x 4096: one in 20.4 us
+    // against one in 24.7)
+    const int64_t pairs = num_sms() / 2, mt = ceil_div(L.M, 256);
+    const int64_t wide = ceil_div(mt * ceil_div(L.N, 256), pairs), narrow = ceil_div(mt * ceil_div(L.N, 128), pairs);
+    if (narrow * 3 < wide * 4)
+        return launch_block_pair<BlockPairCfg<128, 7>>(L);
+    return launch_block_pair<BlockPairCfg<256, 5>>(L);
 }
 
 // Shapes, types and pointers of a block-scaled linear layer, activations aside.

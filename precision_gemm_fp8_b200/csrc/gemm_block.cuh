@@ -57,6 +57,18 @@ template <int BN_, int STAGES_, int NBUF_> struct BlockCfg {
     static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 };
 
+// Bounded wait for a barrier that another role of the kernel completes within
+// a k-block's time, on every k-block.  The first polls read no clock: the
+// timer takes longer to read than such a wait lasts, and the read would sit
+// between two roles that hand a buffer to one another.  Then as wait_bounded.
+__device__ __forceinline__ bool wait_step(uint64_t *bar, uint32_t parity, volatile int *abort)
+{
+    for (int i = 0; i < 64; ++i)
+        if (mbar_try_wait(bar, parity))
+            return true;
+    return wait_bounded(bar, parity, abort);
+}
+
 struct BlockCtl {
     uint64_t full[8];
     uint64_t empty[8];
@@ -101,6 +113,17 @@ __device__ __forceinline__ void store_out4(void *y, int64_t i, float4 v, int dt)
     } else {
         *reinterpret_cast<float4 *>(static_cast<float *>(y) + i) = v;
     }
+}
+
+// Two outputs of a 16-bit type in one word.
+__device__ __forceinline__ uint32_t pack_out2(float2 v, int dt)
+{
+    if (dt == 2) {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y);
+        return *reinterpret_cast<const uint32_t *>(&a);
+    }
+    const __half2 a = __floats2half2_rn(v.x, v.y);
+    return *reinterpret_cast<const uint32_t *>(&a);
 }
 
 // Adds accumulator columns [0, BN) of this thread's row (tensor memory at
@@ -193,7 +216,7 @@ __global__ void __launch_bounds__(C::kThreads)
             uint32_t ph = 0;
             int issued = first;
             for (int kb = kb0 + first; kb < kb1; ++kb) {
-                if (!wait_bounded(&ctl->empty[s], ph, abort_flag))
+                if (!wait_step(&ctl->empty[s], ph, abort_flag))
                     break;
                 uint8_t *st = smem + s * C::kStage;
                 mbar_arrive_expect_tx(&ctl->full[s], C::kStage);
@@ -215,26 +238,28 @@ __global__ void __launch_bounds__(C::kThreads)
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
         grid_dependency_wait();
-        if (lane == 0) {
+        {
             constexpr uint32_t idesc = make_idesc(128, BN, 0, 0);
             int s = 0, b = 0;
             uint32_t ph = 0, bph = 1;
             bool ok = true;
             for (int kb = kb0; kb < kb1; ++kb) {
-                if (!wait_bounded(&ctl->acc_empty[b], bph, abort_flag) ||
-                    !wait_bounded(&ctl->full[s], ph, abort_flag)) {
-                    ok = false;
+                ok = wait_step(&ctl->acc_empty[b], bph, abort_flag) && wait_step(&ctl->full[s], ph, abort_flag);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok)
                     break;
-                }
                 tc_fence_after();
                 const uint32_t a_addr = smem_u32(smem + s * C::kStage);
                 const uint32_t b_addr = a_addr + C::kTileA;
+                if (elect_one()) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    umma_f8f6f4(tmem + b * BN, sdesc_sw128(a_addr + k * 32), sdesc_sw128(b_addr + k * 32), idesc,
-                                k > 0 ? 1u : 0u);
-                umma_commit(&ctl->empty[s]);
-                umma_commit(&ctl->acc_full[b]);
+                    for (int k = 0; k < 4; ++k)
+                        umma_f8f6f4(tmem + b * BN, sdesc_sw128(a_addr + k * 32), sdesc_sw128(b_addr + k * 32), idesc,
+                                    k > 0 ? 1u : 0u);
+                    umma_commit(&ctl->empty[s]);
+                    umma_commit(&ctl->acc_full[b]);
+                }
+                __syncwarp();
                 if (++s == STAGES) {
                     s = 0;
                     ph ^= 1u;
@@ -244,7 +269,7 @@ __global__ void __launch_bounds__(C::kThreads)
                     bph ^= 1u;
                 }
             }
-            if (!ok) {
+            if (!ok && elect_one()) {
                 umma_commit(&ctl->drain);
                 wait_drain(&ctl->drain, 0);
             }
@@ -290,7 +315,7 @@ __global__ void __launch_bounds__(C::kThreads)
                 fetch(kb0 + i + kScaleChunk);
                 bar_sync_warps2to5();
             }
-            ok = ok && wait_bounded(&ctl->acc_full[b], bph, abort_flag);
+            ok = ok && wait_step(&ctl->acc_full[b], bph, abort_flag);
             ok = __all_sync(0xffffffffu, ok);
             if (ok) {
                 tc_fence_after();

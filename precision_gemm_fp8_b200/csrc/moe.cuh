@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(C::kThreads)
             int s = 0, issued = 0;
             uint32_t ph = 1;
             for (int kb = kb0; kb < kb1; ++kb) {
-                if (!wait_bounded(&ctl->empty[s], ph, abort_flag))
+                if (!wait_step(&ctl->empty[s], ph, abort_flag))
                     break;
                 uint8_t *st = smem + s * C::kStage;
                 mbar_arrive_expect_tx(&ctl->full[s], C::kStage);
@@ -369,28 +369,30 @@ __global__ void __launch_bounds__(C::kThreads)
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
-        if (lane == 0) {
+        {
             constexpr uint32_t idesc = make_idesc(128, BN, 0, 0);
             int s = 0, b = 0;
             uint32_t ph = 0, bph = 1;
             bool ok = true;
             for (int kb = kb0; kb < kb1; ++kb) {
-                if (!wait_bounded(&ctl->acc_empty[b], bph, abort_flag) ||
-                    !wait_bounded(&ctl->full[s], ph, abort_flag)) {
-                    ok = false;
+                ok = wait_step(&ctl->acc_empty[b], bph, abort_flag) && wait_step(&ctl->full[s], ph, abort_flag);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok)
                     break;
-                }
                 tc_fence_after();
                 const uint32_t a_addr = smem_u32(smem + s * C::kStage);
                 const uint32_t x_addr = a_addr + 2 * C::kTileA;
+                if (elect_one()) {
 #pragma unroll
-                for (int half = 0; half < 2; ++half)
+                    for (int half = 0; half < 2; ++half)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        umma_f8f6f4(tmem + (b * 2 + half) * BN, sdesc_sw128(a_addr + half * C::kTileA + k * 32),
-                                    sdesc_sw128(x_addr + k * 32), idesc, k > 0 ? 1u : 0u);
-                umma_commit(&ctl->empty[s]);
-                umma_commit(&ctl->acc_full[b]);
+                        for (int k = 0; k < 4; ++k)
+                            umma_f8f6f4(tmem + (b * 2 + half) * BN, sdesc_sw128(a_addr + half * C::kTileA + k * 32),
+                                        sdesc_sw128(x_addr + k * 32), idesc, k > 0 ? 1u : 0u);
+                    umma_commit(&ctl->empty[s]);
+                    umma_commit(&ctl->acc_full[b]);
+                }
+                __syncwarp();
                 if (++s == STAGES) {
                     s = 0;
                     ph ^= 1u;
@@ -400,7 +402,7 @@ __global__ void __launch_bounds__(C::kThreads)
                     bph ^= 1u;
                 }
             }
-            if (!ok) {
+            if (!ok && elect_one()) {
                 umma_commit(&ctl->drain);
                 wait_drain(&ctl->drain, 0);
             }
@@ -449,7 +451,7 @@ __global__ void __launch_bounds__(C::kThreads)
                 fetch(kb0 + i + CH);
                 bar_sync_warps2to5();
             }
-            ok = ok && wait_bounded(&ctl->acc_full[b], bph, abort_flag);
+            ok = ok && wait_step(&ctl->acc_full[b], bph, abort_flag);
             ok = __all_sync(0xffffffffu, ok);
             if (ok) {
                 tc_fence_after();
@@ -655,7 +657,7 @@ __global__ void __launch_bounds__(C::kThreads)
             uint32_t ph = 0;
             int a = (u0 + first) / p.fblocks, kb = (u0 + first) % p.fblocks;
             for (int u = u0 + first; u < u1; ++u) {
-                if (!wait_bounded(&ctl->empty[s], ph, abort_flag))
+                if (!wait_step(&ctl->empty[s], ph, abort_flag))
                     break;
                 load_w(s, a, kb);
                 load_h(s, a, kb);
@@ -678,27 +680,29 @@ __global__ void __launch_bounds__(C::kThreads)
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
         grid_dependency_wait();
-        if (lane == 0) {
+        {
             int s = 0, b = 0;
             uint32_t ph = 0, bph = 1;
             bool ok = true;
             int a = u0 / p.fblocks, kb = u0 % p.fblocks;
             for (int u = u0; u < u1; ++u) {
-                if (!wait_bounded(&ctl->acc_empty[b], bph, abort_flag) ||
-                    !wait_bounded(&ctl->full[s], ph, abort_flag)) {
-                    ok = false;
+                ok = wait_step(&ctl->acc_empty[b], bph, abort_flag) && wait_step(&ctl->full[s], ph, abort_flag);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok)
                     break;
-                }
                 tc_fence_after();
                 const uint32_t idesc = make_idesc(128, tokens16(experts[a].z), 0, 0);
                 const uint32_t a_addr = smem_u32(smem + s * C::kStage);
                 const uint32_t h_addr = a_addr + C::kTileA;
+                if (elect_one()) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    umma_f8f6f4(tmem + b * BN, sdesc_sw128(a_addr + k * 32), sdesc_sw128(h_addr + k * 32), idesc,
-                                k > 0 ? 1u : 0u);
-                umma_commit(&ctl->empty[s]);
-                umma_commit(&ctl->acc_full[b]);
+                    for (int k = 0; k < 4; ++k)
+                        umma_f8f6f4(tmem + b * BN, sdesc_sw128(a_addr + k * 32), sdesc_sw128(h_addr + k * 32), idesc,
+                                    k > 0 ? 1u : 0u);
+                    umma_commit(&ctl->empty[s]);
+                    umma_commit(&ctl->acc_full[b]);
+                }
+                __syncwarp();
                 if (++kb == p.fblocks) {
                     kb = 0;
                     ++a;
@@ -712,7 +716,7 @@ __global__ void __launch_bounds__(C::kThreads)
                     bph ^= 1u;
                 }
             }
-            if (!ok) {
+            if (!ok && elect_one()) {
                 umma_commit(&ctl->drain);
                 wait_drain(&ctl->drain, 0);
             }
@@ -763,7 +767,7 @@ __global__ void __launch_bounds__(C::kThreads)
                 fetch(u0 + i + kScaleChunk);
                 bar_sync_warps2to5();
             }
-            ok = ok && wait_bounded(&ctl->acc_full[b], bph, abort_flag);
+            ok = ok && wait_step(&ctl->acc_full[b], bph, abort_flag);
             ok = __all_sync(0xffffffffu, ok);
             const int rows = experts[a].z;
             if (ok) {
