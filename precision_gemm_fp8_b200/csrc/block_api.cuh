@@ -79,10 +79,11 @@ struct BlockLaunch {
     cudaStream_t stream;
 };
 
-// K-split of the weight-streaming kernel: the largest cluster that keeps the
-// grid within `slots` CTAs (all of them resident at once, so that none waits
-// for a second round while the others hold the memory system) and leaves at
-// least four k-blocks to a CTA.
+// K-split of the weight-streaming kernels: the largest cluster that keeps the
+// grid within `slots` CTAs, all of them resident at once with SMs to spare
+// (one token, 12288 x 4096, 96 tiles: 12.9 us at 2, 16.3 at 3 with 288 of 296
+// places taken, 13.9 at 1; 64 tiles of 8192 x 28672: 38.4 at 4, 44.0 at 6), and
+// leaves at least four k-blocks to a CTA.
 static int block_splits(int64_t tiles, int64_t kblocks, int64_t slots)
 {
     static const int kSizes[] = {8, 6, 4, 3, 2};
@@ -106,6 +107,9 @@ static BlockParams block_params(const BlockLaunch &L)
     p.ydt = L.ydt;
     return p;
 }
+
+// CTAs that the grid of a weight-streaming kernel may have, at one or two to an SM.
+static int64_t block_slots(int ctas_per_sm) { return ctas_per_sm == 1 ? num_sms() : num_sms() * 7 / 4; }
 
 template <class C> static bool block_maps(const BlockLaunch &L, CUtensorMap &tmX, CUtensorMap &tmW)
 {
@@ -135,7 +139,7 @@ template <class C> static pgf8_status launch_block(const BlockLaunch &L, int cta
     const int64_t nt = ceil_div(L.N, 128), mt = ceil_div(L.M, C::BN);
     if (mt > 65535)
         return PGF8_ERR_UNSUPPORTED;   // the grid's y extent
-    const int splits = block_splits(nt * mt, p.kblocks, static_cast<int64_t>(ctas_per_sm) * num_sms());
+    const int splits = block_splits(nt * mt, p.kblocks, block_slots(ctas_per_sm));
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof(cfg));
     cfg.gridDim = dim3(static_cast<unsigned>(nt), static_cast<unsigned>(mt), static_cast<unsigned>(splits));

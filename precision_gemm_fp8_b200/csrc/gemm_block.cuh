@@ -18,8 +18,11 @@
 //
 //   warp 0      TMA producer: STAGES-deep ring of (weight tile, token tile)
 //   warp 1      tensor-memory allocation, MMA issue (one thread)
-//   warps 2-5   scales, accumulation over k-blocks, output: thread r holds
-//               weight row r of the tile, BN tokens
+//   warps 2...  scales, accumulation over k-blocks, output: four warps for
+//               every 32 tokens, a thread holding one weight row's sums for
+//               them (16 at BN = 16).  With one warp a lane quadrant for 128
+//               tokens a k-block took about 1000 cycles of one warp's time
+//               against the MMA's 256, and the layer was bound by it.
 // Waits are bounded as in gemm.cuh; after a wait that gave up the epilogue
 // warps keep walking their loop without touching tensor memory, so that
 // their barriers stay matched.
@@ -27,6 +30,8 @@
 
 #include "gemm.cuh"
 #include "packed_ptx.cuh"
+
+#include <cstddef>
 
 namespace pgf8 {
 
@@ -38,7 +43,9 @@ template <int BN_, int STAGES_, int NBUF_> struct BlockCfg {
     static constexpr int NBUF = NBUF_;   // accumulator buffers of BN columns
     static constexpr int KIND = kE4M3;
     static constexpr int XQ = 0;
-    static constexpr int kThreads = 192;
+    static constexpr int COLS = BN < 32 ? BN : 32;       // tokens of an epilogue thread
+    static constexpr int kEpi = 128 * (BN / COLS);       // epilogue threads
+    static constexpr int kThreads = 64 + kEpi;
     static constexpr int kTileA = 128 * 128;
     static constexpr int kStage = kTileA + BN * 128;
     static constexpr int kRowsW = 128;
@@ -67,6 +74,39 @@ __device__ __forceinline__ bool wait_step(uint64_t *bar, uint32_t parity, volati
         if (mbar_try_wait(bar, parity))
             return true;
     return wait_bounded(bar, parity, abort);
+}
+
+// The same by 32-bit shared-memory addresses, for loops short of registers.
+__device__ __forceinline__ bool mbar_try_wait_at(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+__device__ __forceinline__ bool wait_step_at(uint32_t bar, uint32_t parity, volatile int *abort)
+{
+    if (mbar_try_wait_at(bar, parity))
+        return true;
+    return wait_step(static_cast<uint64_t *>(__cvta_shared_to_generic(bar)), parity, abort);
+}
+
+__device__ __forceinline__ void mbar_arrive_at(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ float ld_shared_f32(uint32_t addr)
+{
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
 }
 
 struct BlockCtl {
@@ -126,29 +166,33 @@ __device__ __forceinline__ uint32_t pack_out2(float2 v, int dt)
     return *reinterpret_cast<const uint32_t *>(&a);
 }
 
-// Adds accumulator columns [0, BN) of this thread's row (tensor memory at
-// taddr) times their scales (shared memory, 16-byte aligned) to acc.
-template <int BN>
-__device__ __forceinline__ void add_scaled(uint32_t taddr, const float *sc, uint64_t (&acc)[BN / 2])
+// Adds COLS accumulator columns of this thread's row (tensor memory at taddr)
+// times their scales (shared memory, 16-byte aligned) to acc.  Single multiply-
+// adds: the packed form (two to an instruction) needs register pairs, and the
+// moves and spills that they brought took more time than it saved.
+template <int COLS>
+__device__ __forceinline__ void add_scaled(uint32_t taddr, const float *sc, float (&acc)[COLS])
 {
-    constexpr int W = BN < 32 ? 16 : 32;
 #pragma unroll
-    for (int c0 = 0; c0 < BN; c0 += W) {
-        uint32_t v[W];
-        if constexpr (W == 32)
-            tmem_ld_32x32b_x32(taddr + c0, v);
-        else
-            tmem_ld_32x32b_x16(taddr + c0, v);
+    for (int c0 = 0; c0 < COLS; c0 += 16) {
+        uint32_t v[16];
+        tmem_ld_32x32b_x16(taddr + c0, v);
         tmem_ld_wait();
-        const ulonglong2 *s = reinterpret_cast<const ulonglong2 *>(sc + c0);
 #pragma unroll
-        for (int j = 0; j < W / 4; ++j) {
-            const ulonglong2 t = s[j];
-            acc[c0 / 2 + 2 * j] = fma_f32x2(pack_f32x2(v[4 * j], v[4 * j + 1]), t.x, acc[c0 / 2 + 2 * j]);
-            acc[c0 / 2 + 2 * j + 1] = fma_f32x2(pack_f32x2(v[4 * j + 2], v[4 * j + 3]), t.y,
-                                                acc[c0 / 2 + 2 * j + 1]);
+        for (int j = 0; j < 16; j += 4) {
+            const float4 t = *reinterpret_cast<const float4 *>(sc + c0 + j);
+            acc[c0 + j] = fmaf(__uint_as_float(v[j]), t.x, acc[c0 + j]);
+            acc[c0 + j + 1] = fmaf(__uint_as_float(v[j + 1]), t.y, acc[c0 + j + 1]);
+            acc[c0 + j + 2] = fmaf(__uint_as_float(v[j + 2]), t.z, acc[c0 + j + 2]);
+            acc[c0 + j + 3] = fmaf(__uint_as_float(v[j + 3]), t.w, acc[c0 + j + 3]);
         }
     }
+}
+
+// Named barrier 1 over the N epilogue threads.
+template <int N> __device__ __forceinline__ void bar_sync_epilogue()
+{
+    asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory");
 }
 
 template <class C>
@@ -180,7 +224,7 @@ __global__ void __launch_bounds__(C::kThreads)
         }
         for (int b = 0; b < NBUF; ++b) {
             mbar_init(&ctl->acc_full[b], 1);
-            mbar_init(&ctl->acc_empty[b], 4);
+            mbar_init(&ctl->acc_empty[b], C::kEpi / 32);
         }
         mbar_init(&ctl->drain, 1);
         ctl->abort = 0;
@@ -277,29 +321,33 @@ __global__ void __launch_bounds__(C::kThreads)
         __syncwarp();
     }
 
-    uint64_t acc[BN / 2];
+    constexpr int COLS = C::COLS, EPI = C::kEpi;
+    float acc[COLS];
     const int qd = warp & 3;
     const int r = qd * 32 + lane;
+    const int col0 = ((warp - 2) >> 2) * COLS;   // this warp's tokens of the tile
     if (warp >= 2) {
         // ------------------------------------------------------------ scales and accumulation
         grid_dependency_wait();   // the token scales come from the kernel before
 #pragma unroll
-        for (int j = 0; j < BN / 2; ++j)
-            acc[j] = 0;
-        const uint32_t t_row = tmem + (static_cast<uint32_t>(qd * 32) << 16);
+        for (int j = 0; j < COLS; ++j)
+            acc[j] = 0.0f;
+        const uint32_t t_row = tmem + (static_cast<uint32_t>(qd * 32) << 16) + static_cast<uint32_t>(col0);
         const int et = static_cast<int>(threadIdx.x) - 64;
-        // sa[m, kb] * sw[n0 / 128, kb] of 8 k-blocks from kb: thread et's values are
-        // tokens (et + 128 i) / 8 at k-block kb + et % 8 (32 contiguous bytes a token)
-        constexpr int PER = BN * kScaleChunk / 128;
-        float pre[PER];
+        // sa[m, kb] and sw[n0 / 128, kb] of 8 k-blocks from kb: thread et's values are
+        // tokens (et + EPI i) / 8 at k-block kb + et % 8 (32 contiguous bytes a token),
+        // loaded a chunk ahead and multiplied when they are stored: a product taken
+        // where they are loaded would wait for the loads
+        constexpr int PER = BN * kScaleChunk / EPI;
+        float pre[PER], wgt = 0.0f;
         const float *swr = p.sw + static_cast<int64_t>(blockIdx.x) * p.kblocks;
         auto fetch = [&](int kb) {
             const int k = kb + (et & 7);
-            const float w = k < kb1 ? __ldg(swr + k) : 0.0f;
+            wgt = k < kb1 ? __ldg(swr + k) : 0.0f;
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
-                const int m = m0 + ((et + 128 * i) >> 3);
-                pre[i] = (k < kb1 && m < p.M) ? p.sa[static_cast<int64_t>(m) * p.kblocks + k] * w : 0.0f;
+                const int m = m0 + ((et + EPI * i) >> 3);
+                pre[i] = (k < kb1 && m < p.M) ? p.sa[static_cast<int64_t>(m) * p.kblocks + k] : 0.0f;
             }
         };
         fetch(kb0);
@@ -311,15 +359,16 @@ __global__ void __launch_bounds__(C::kThreads)
             if (i % kScaleChunk == 0) {
 #pragma unroll
                 for (int j = 0; j < PER; ++j)
-                    buf[(et & 7) * C::kScalePitch + ((et + 128 * j) >> 3)] = pre[j];
-                fetch(kb0 + i + kScaleChunk);
-                bar_sync_warps2to5();
+                    buf[(et & 7) * C::kScalePitch + ((et + EPI * j) >> 3)] = pre[j] * wgt;
+                if (i + kScaleChunk < kb1 - kb0)
+                    fetch(kb0 + i + kScaleChunk);
+                bar_sync_epilogue<EPI>();
             }
             ok = ok && wait_step(&ctl->acc_full[b], bph, abort_flag);
             ok = __all_sync(0xffffffffu, ok);
             if (ok) {
                 tc_fence_after();
-                add_scaled<BN>(t_row + b * BN, buf + (i % kScaleChunk) * C::kScalePitch, acc);
+                add_scaled<COLS>(t_row + b * BN, buf + (i % kScaleChunk) * C::kScalePitch + col0, acc);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
@@ -338,12 +387,10 @@ __global__ void __launch_bounds__(C::kThreads)
     if (splits == 1) {
         if (warp >= 2 && n < p.N) {
 #pragma unroll
-            for (int c = 0; c < BN; c += 2) {
-                const float2 v = unpack_f32x2(acc[c / 2]);
-                if (m0 + c < p.M)
-                    store_out(p.y, static_cast<int64_t>(m0 + c) * p.N + n, v.x, p.ydt);
-                if (m0 + c + 1 < p.M)
-                    store_out(p.y, static_cast<int64_t>(m0 + c + 1) * p.N + n, v.y, p.ydt);
+            for (int c = 0; c < COLS; ++c) {
+                const int m = m0 + col0 + c;
+                if (m < p.M)
+                    store_out(p.y, static_cast<int64_t>(m) * p.N + n, acc[c], p.ydt);
             }
         }
         tc_fence_before();
@@ -357,11 +404,8 @@ __global__ void __launch_bounds__(C::kThreads)
         __syncthreads();
         if (warp >= 2) {
 #pragma unroll
-            for (int c = 0; c < BN; c += 2) {
-                const float2 v = unpack_f32x2(acc[c / 2]);
-                part[c * 128 + r] = v.x;
-                part[(c + 1) * 128 + r] = v.y;
-            }
+            for (int c = 0; c < COLS; ++c)
+                part[(col0 + c) * 128 + r] = acc[c];
         }
         cluster_sync_all();
         if (warp >= 2) {
@@ -369,7 +413,8 @@ __global__ void __launch_bounds__(C::kThreads)
             // flight together and go out as one store
             const int n4 = n0 + lane * 4;
             const uint32_t base = smem_u32(part) + lane * 16;
-            for (int c = static_cast<int>(blockIdx.z) + splits * (warp - 2); n4 < p.N && c < cols; c += 4 * splits) {
+            for (int c = static_cast<int>(blockIdx.z) + splits * (warp - 2); n4 < p.N && c < cols;
+                 c += EPI / 32 * splits) {
                 float4 t[8];
 #pragma unroll
                 for (int z = 0; z < 8; ++z)

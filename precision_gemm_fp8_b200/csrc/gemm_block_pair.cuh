@@ -54,12 +54,12 @@ template <int BN_, int STAGES_> struct BlockPairCfg {
 // memory whose loads have completed (tcgen05.wait::ld), no shared or global
 // data.  With .release.cluster the odd CTA's eight arrivals per k-block each
 // waited for a cluster-wide fence, 1.5 thousand cycles a k-block.
-__device__ __forceinline__ void mbar_arrive_cta0(uint64_t *bar)
+__device__ __forceinline__ void mbar_arrive_cta0(uint32_t bar)
 {
     asm volatile(
         "{\n\t.reg .b32 ra;\n\t"
         "mapa.shared::cluster.u32 ra, %0, 0;\n\t"
-        "mbarrier.arrive.shared::cluster.b64 _, [ra];\n\t}\n" ::"r"(smem_u32(bar))
+        "mbarrier.arrive.shared::cluster.b64 _, [ra];\n\t}\n" ::"r"(bar)
         : "memory");
 }
 
@@ -136,19 +136,22 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         const int qd = warp & 3;
         const int quarter = (warp - 4) >> 2;
         const uint32_t t_row = tmem + (static_cast<uint32_t>(qd * 32) << 16) + static_cast<uint32_t>(quarter * COLS);
-        const float *const my_scale = scales + (quarter * COLS / 128) * 128 + qd * 32 + lane;
-        int b = 0, slot = 0;
-        uint32_t bph = 0, sph = 0;
+        const uint32_t my_scale = smem_u32(scales + (quarter * COLS / 128) * 128 + qd * 32 + lane);
+        const uint32_t bars = smem_u32(ctl);
+        uint32_t it = 0;                          // k-blocks so far: buffers, slots and phases follow from it
         bool ok = true;
         for (int t = pair; t < total; t += npairs) {
             float acc[COLS];
 #pragma unroll
             for (int j = 0; j < COLS; ++j)
                 acc[j] = 0.0f;
-            for (int kb = 0; kb < p.kblocks; ++kb) {
-                ok = wait_step(&ctl->scale_full[slot], sph, abort_flag);
-                const float f = my_scale[slot * C::kBlocks * 128];
-                ok = ok && wait_step(&ctl->acc_full[b], bph, abort_flag);
+            for (int kb = 0; kb < p.kblocks; ++kb, ++it) {
+                const uint32_t b = it % C::NBUF, slot = it % C::kScaleSlots;
+                ok = wait_step_at(bars + offsetof(BlockPairCtl, scale_full) + slot * 8, (it / C::kScaleSlots) & 1,
+                                  abort_flag);
+                const float f = ld_shared_f32(my_scale + slot * C::kBlocks * 512);
+                ok = ok && wait_step_at(bars + offsetof(BlockPairCtl, acc_full) + b * 8, (it / C::NBUF) & 1,
+                                        abort_flag);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok)
                     break;
@@ -163,21 +166,13 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) {
-                            mbar_arrive_cta0(&ctl->acc_empty[b]);
-                            mbar_arrive(&ctl->scale_empty[slot]);
+                            mbar_arrive_cta0(bars + offsetof(BlockPairCtl, acc_empty) + b * 8);
+                            mbar_arrive_at(bars + offsetof(BlockPairCtl, scale_empty) + slot * 8);
                         }
                     }
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
                         acc[c + i] = fmaf(__uint_as_float(v[i]), f, acc[c + i]);
-                }
-                if (++b == NBUF) {
-                    b = 0;
-                    bph ^= 1u;
-                }
-                if (++slot == C::kScaleSlots) {
-                    slot = 0;
-                    sph ^= 1u;
                 }
             }
             if (!ok)

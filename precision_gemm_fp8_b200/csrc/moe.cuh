@@ -256,16 +256,19 @@ __global__ void __launch_bounds__(kMoePlanThreads) moe_plan_kernel(const MoeRout
 }
 
 // ------------------------------------------------------------------ gate + up
-template <int BN_, int STAGES_, int NBUF_> struct MoeUpCfg {
+template <int BN_, int STAGES_, int NBUF_, int CTAS_> struct MoeUpCfg {
     static constexpr int BN = BN_;
     static constexpr int STAGES = STAGES_;
+    static constexpr int CTAS = CTAS_;                 // per SM
     static constexpr int NBUF = NBUF_;                 // buffers of 2 BN columns (gate, up)
-    static constexpr int kThreads = 192;
+    static constexpr int COLS = BN < 32 ? BN : 32;     // tokens of an epilogue thread
+    static constexpr int kEpi = 128 * (BN / COLS);     // epilogue threads
+    static constexpr int kThreads = 64 + kEpi;
     static constexpr int kTileA = 128 * 128;
     static constexpr int kStage = 2 * kTileA + BN * 128;
     static constexpr int kTmemCols = NBUF * 2 * BN;
     static constexpr int kRingBytes = STAGES * kStage; // reused for the partial tiles [2][BN][128] f32
-    static constexpr int kChunk = BN == 16 ? 8 : 4;    // k-blocks of scales staged at a time
+    static constexpr int kChunk = BN == 32 ? 4 : 8;    // k-blocks of scales staged at a time
     static constexpr int kScalePitch = BN + 4;
     static constexpr int kScaleOffset = kRingBytes;
     static constexpr int kScaleBytes = 2 * 2 * kChunk * kScalePitch * 4;
@@ -275,7 +278,7 @@ template <int BN_, int STAGES_, int NBUF_> struct MoeUpCfg {
     static_assert(STAGES <= 8 && NBUF <= 8, "barriers");
     static_assert((kTmemCols & (kTmemCols - 1)) == 0 && kTmemCols >= 32 && kTmemCols <= 256, "tensor memory");
     static_assert(kRingBytes >= 2 * BN * 128 * 4, "partial tiles");
-    static_assert(2 * (kSmemBytes + 1024) <= 228 * 1024, "two CTAs per SM");
+    static_assert(kSmemBytes <= 227 * 1024 && CTAS * (kSmemBytes + 1024) <= 228 * 1024, "shared memory");
 };
 
 struct MoeUpParams {
@@ -290,7 +293,7 @@ struct MoeUpParams {
 // Grid (fblocks, min(E, T k), splits): cluster of `splits` CTAs along z for
 // 128 hidden features of one chosen expert, each a range of k-blocks of H.
 template <class C>
-__global__ void __launch_bounds__(C::kThreads)
+__global__ void __launch_bounds__(C::kThreads, C::CTAS)
     moe_gate_up_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                        const MoeUpParams p)
 {
@@ -324,7 +327,7 @@ __global__ void __launch_bounds__(C::kThreads)
         }
         for (int b = 0; b < NBUF; ++b) {
             mbar_init(&ctl->acc_full[b], 1);
-            mbar_init(&ctl->acc_empty[b], 4);
+            mbar_init(&ctl->acc_empty[b], C::kEpi / 32);
         }
         mbar_init(&ctl->drain, 1);
         ctl->abort = 0;
@@ -410,18 +413,21 @@ __global__ void __launch_bounds__(C::kThreads)
         __syncwarp();
     }
 
-    uint64_t accg[BN / 2], accu[BN / 2];
+    constexpr int COLS = C::COLS, EPI = C::kEpi;
+    float accg[COLS], accu[COLS];
     const int qd = warp & 3;
     const int r = qd * 32 + lane;
+    const int col0 = ((warp - 2) >> 2) * COLS;   // this warp's tokens
     if (warp >= 2) {
         // ------------------------------------------------------------ scales and accumulation
 #pragma unroll
-        for (int j = 0; j < BN / 2; ++j)
-            accg[j] = accu[j] = 0;
-        const uint32_t t_row = tmem + (static_cast<uint32_t>(qd * 32) << 16);
+        for (int j = 0; j < COLS; ++j)
+            accg[j] = accu[j] = 0.0f;
+        const uint32_t t_row = tmem + (static_cast<uint32_t>(qd * 32) << 16) + static_cast<uint32_t>(col0);
         const int et = static_cast<int>(threadIdx.x) - 64;
-        constexpr int CH = C::kChunk, PER = BN * CH / 128;
-        float pre[PER], wg, wu;
+        // as in gemm_block.cuh: loaded a chunk ahead, multiplied when stored
+        constexpr int CH = C::kChunk, PER = BN * CH / EPI;
+        float pre[PER], wg = 0.0f, wu = 0.0f;
         const float *swg = p.s13 + (static_cast<int64_t>(ex.x) * 2 * p.fblocks + blockIdx.x) * p.hblocks;
         const float *swu = swg + static_cast<int64_t>(p.fblocks) * p.hblocks;
         auto fetch = [&](int kb) {
@@ -430,7 +436,7 @@ __global__ void __launch_bounds__(C::kThreads)
             wu = k < kb1 ? __ldg(swu + k) : 0.0f;
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
-                const int t = (et + 128 * i) / CH;
+                const int t = (et + EPI * i) / CH;
                 pre[i] = (k < kb1 && t < p.T) ? __ldcg(p.sx + t * p.hblocks + k) : 0.0f;
             }
         };
@@ -444,20 +450,21 @@ __global__ void __launch_bounds__(C::kThreads)
             if (i % CH == 0) {
 #pragma unroll
                 for (int j = 0; j < PER; ++j) {
-                    const int at = (et & (CH - 1)) * C::kScalePitch + ((et + 128 * j) / CH);
+                    const int at = (et & (CH - 1)) * C::kScalePitch + ((et + EPI * j) / CH);
                     bufg[at] = pre[j] * wg;
                     bufu[at] = pre[j] * wu;
                 }
-                fetch(kb0 + i + CH);
-                bar_sync_warps2to5();
+                if (i + CH < kb1 - kb0)
+                    fetch(kb0 + i + CH);
+                bar_sync_epilogue<EPI>();
             }
             ok = ok && wait_step(&ctl->acc_full[b], bph, abort_flag);
             ok = __all_sync(0xffffffffu, ok);
             if (ok) {
                 tc_fence_after();
-                const int at = (i % CH) * C::kScalePitch;
-                add_scaled<BN>(t_row + b * 2 * BN, bufg + at, accg);
-                add_scaled<BN>(t_row + b * 2 * BN + BN, bufu + at, accu);
+                const int at = (i % CH) * C::kScalePitch + col0;
+                add_scaled<COLS>(t_row + b * 2 * BN, bufg + at, accg);
+                add_scaled<COLS>(t_row + b * 2 * BN + BN, bufu + at, accu);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
@@ -477,12 +484,9 @@ __global__ void __launch_bounds__(C::kThreads)
     __syncthreads();   // the ring is idle
     if (warp >= 2) {
 #pragma unroll
-        for (int c = 0; c < BN; c += 2) {
-            const float2 g = unpack_f32x2(accg[c / 2]), u = unpack_f32x2(accu[c / 2]);
-            part[c * 128 + r] = g.x;
-            part[(c + 1) * 128 + r] = g.y;
-            part[(BN + c) * 128 + r] = u.x;
-            part[(BN + c + 1) * 128 + r] = u.y;
+        for (int c = 0; c < COLS; ++c) {
+            part[(col0 + c) * 128 + r] = accg[c];
+            part[(BN + col0 + c) * 128 + r] = accu[c];
         }
     }
     if (splits > 1)
@@ -493,24 +497,30 @@ __global__ void __launch_bounds__(C::kThreads)
         // one warp to a row of hidden codes, four features a lane
         const uint32_t base = smem_u32(part) + lane * 16;
         const int f = f0 + lane * 4;
-        for (int i = static_cast<int>(blockIdx.z) + splits * (warp - 2); i < ex.z; i += 4 * splits) {
+        for (int i = static_cast<int>(blockIdx.z) + splits * (warp - 2); i < ex.z; i += EPI / 32 * splits) {
             const int row = ex.y + i;
             const uint32_t off = base + __ldcg(p.plan.tok + row) * 512;
-            float4 tg[8], tu[8];
+            // the partials in rank order, four ranks in flight at a time
+            float4 g = make_float4(0.0f, 0.0f, 0.0f, 0.0f), u = g;
 #pragma unroll
-            for (int z = 0; z < 8; ++z)
-                if (z < splits) {
-                    const uint32_t a = splits > 1 ? map_shared_rank(off, static_cast<uint32_t>(z)) : off;
-                    tg[z] = ld_shared_cluster_v4_relaxed(a);
-                    tu[z] = ld_shared_cluster_v4_relaxed(a + BN * 512);
-                }
-            float4 g = tg[0], u = tu[0];
+            for (int z0 = 0; z0 < 8; z0 += 4) {
+                if (z0 >= splits)
+                    break;
+                float4 tg[4], tu[4];
 #pragma unroll
-            for (int z = 1; z < 8; ++z)
-                if (z < splits) {
-                    g = make_float4(g.x + tg[z].x, g.y + tg[z].y, g.z + tg[z].z, g.w + tg[z].w);
-                    u = make_float4(u.x + tu[z].x, u.y + tu[z].y, u.z + tu[z].z, u.w + tu[z].w);
-                }
+                for (int z = 0; z < 4; ++z)
+                    if (z0 + z < splits) {
+                        const uint32_t a = splits > 1 ? map_shared_rank(off, static_cast<uint32_t>(z0 + z)) : off;
+                        tg[z] = ld_shared_cluster_v4_relaxed(a);
+                        tu[z] = ld_shared_cluster_v4_relaxed(a + BN * 512);
+                    }
+#pragma unroll
+                for (int z = 0; z < 4; ++z)
+                    if (z0 + z < splits) {
+                        g = make_float4(g.x + tg[z].x, g.y + tg[z].y, g.z + tg[z].z, g.w + tg[z].w);
+                        u = make_float4(u.x + tu[z].x, u.y + tu[z].y, u.z + tu[z].z, u.w + tu[z].w);
+                    }
+            }
             const bool live = f < p.F;   // F % 16 == 0: a lane's four features exist together
             float h[4] = {silu_mul(g.x, u.x), silu_mul(g.y, u.y), silu_mul(g.z, u.z), silu_mul(g.w, u.w)};
             float a = 0.0f;
@@ -548,9 +558,9 @@ template <int BN_, int STAGES_, int NBUF_> struct MoeDownCfg {
     static constexpr int kStage = kTileA + BN * 128;
     static constexpr int kTmemCols = NBUF * BN < 32 ? 32 : NBUF * BN;
     static constexpr int kRingBytes = STAGES * kStage;
-    static constexpr int kSumOffset = kRingBytes;        // [BN][128] f32: the output tile, by token
+    static constexpr int kSumOffset = kRingBytes;        // [BN + 1][128] f32: the output tile, by token
     static constexpr int kScalePitch = BN + 4;
-    static constexpr int kScaleOffset = kSumOffset + BN * 512;
+    static constexpr int kScaleOffset = kSumOffset + (BN + 1) * 512;
     static constexpr int kScaleBytes = 2 * kScaleChunk * kScalePitch * 4;
     static constexpr int kCtlOffset = kScaleOffset + kScaleBytes;
     static constexpr int kPlanOffset = kCtlOffset + 512; // experts (int4), tokens, weights: sized at launch
@@ -736,21 +746,23 @@ __global__ void __launch_bounds__(C::kThreads)
         const uint32_t t_row = tmem + (static_cast<uint32_t>(qd * 32) << 16);
         const int et = static_cast<int>(threadIdx.x) - 64;
         constexpr int PER = BN * kScaleChunk / 128;
-        float pre[PER];
-        // sh[row, kb] * s2[e, feature block, kb] of 8 units from u: thread et's
-        // values are the expert's rows (et + 128 i) / 8 at unit u + et % 8
+        float pre[PER], wgt = 0.0f;
+        int pre_row = 0, pre_rows = 0;
+        // sh[row, kb], s2[e, feature block, kb] and the rows' weights of 8 units from u:
+        // thread et's values are the expert's rows (et + 128 i) / 8 at unit u + et % 8
         auto fetch = [&](int u) {
             u += et & 7;
             const bool in = u < u1;
             const int a = in ? u / p.fblocks : 0;
             const int k = in ? u - a * p.fblocks : 0;
             const int4 ex = in ? experts[a] : make_int4(0, 0, 0, 0);
-            const float w =
-                in ? __ldg(p.s2 + (static_cast<int64_t>(ex.x) * gridDim.x + blockIdx.x) * p.fblocks + k) : 0.0f;
+            wgt = in ? __ldg(p.s2 + (static_cast<int64_t>(ex.x) * gridDim.x + blockIdx.x) * p.fblocks + k) : 0.0f;
+            pre_row = ex.y;
+            pre_rows = ex.z;
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
                 const int c = (et + 128 * i) >> 3;
-                pre[i] = c < ex.z ? __ldcg(p.sh + (ex.y + c) * p.fblocks + k) * w : 0.0f;
+                pre[i] = c < ex.z ? __ldcg(p.sh + (ex.y + c) * p.fblocks + k) : 0.0f;
             }
         };
         fetch(u0);
@@ -762,10 +774,13 @@ __global__ void __launch_bounds__(C::kThreads)
             float *buf = sc + ((i / kScaleChunk) & 1) * kScaleChunk * C::kScalePitch;
             if (i % kScaleChunk == 0) {
 #pragma unroll
-                for (int j = 0; j < PER; ++j)
-                    buf[(et & 7) * C::kScalePitch + ((et + 128 * j) >> 3)] = pre[j];
-                fetch(u0 + i + kScaleChunk);
-                bar_sync_warps2to5();
+                for (int j = 0; j < PER; ++j) {
+                    const int c = (et + 128 * j) >> 3;
+                    buf[(et & 7) * C::kScalePitch + c] = c < pre_rows ? pre[j] * wgt * weight[pre_row + c] : 0.0f;
+                }
+                if (i + kScaleChunk < u1 - u0)
+                    fetch(u0 + i + kScaleChunk);
+                bar_sync_epilogue<128>();
             }
             ok = ok && wait_step(&ctl->acc_full[b], bph, abort_flag);
             ok = __all_sync(0xffffffffu, ok);
@@ -795,15 +810,27 @@ __global__ void __launch_bounds__(C::kThreads)
                     mbar_arrive(&ctl->acc_empty[b]);
             }
             if (kb + 1 == p.fblocks || i + 1 == u1 - u0) {
-                // the expert's (or the range's) last unit: to the output tile, by token
+                // the expert's (or the range's) last unit: to the output tile, by token.
+                // Rows of one expert are different tokens, so 16 of them are read
+                // together; columns behind the last row go to a spare row of the tile.
                 const int row0 = experts[a].y;
 #pragma unroll
-                for (int c = 0; c < BN; ++c) {
-                    if (c < rows) {
-                        float *o = sum + tok[row0 + c] * 128 + r;
-                        *o = fmaf(acc[c], weight[row0 + c], *o);
+                for (int c0 = 0; c0 < BN; c0 += 16) {
+                    if (c0 < rows) {
+                        const int mine = c0 + (lane & 15) < rows ? tok[row0 + c0 + (lane & 15)] : BN;
+                        float *o[16];
+                        float v[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            o[j] = sum + __shfl_sync(0xffffffffu, mine, j) * 128 + r;
+                            v[j] = *o[j];
+                        }
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            *o[j] = v[j] + acc[c0 + j];
+                            acc[c0 + j] = 0.0f;
+                        }
                     }
-                    acc[c] = 0.0f;
                 }
             }
             if (++kb == p.fblocks) {

@@ -1,48 +1,11 @@
-// Inline-PTX wrappers of the block-scaled kernels: wide tensor-memory loads
-// and packed binary32 arithmetic.  As in sm100_ptx.cuh, each is one PTX
-// instruction as documented in the PTX ISA for sm_100a.
+// Inline-PTX wrappers of the block-scaled kernels beside those of
+// sm100_ptx.cuh; each is one PTX instruction (or a fixed short sequence) as
+// documented in the PTX ISA for sm_100a.
 #pragma once
 
 #include "sm100_ptx.cuh"
 
 namespace pgf8 {
-
-// 32 lanes x 32 bits, 32 consecutive columns per thread.
-__device__ __forceinline__ void tmem_ld_32x32b_x32(uint32_t taddr, uint32_t (&r)[32])
-{
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32"
-        " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15,"
-        " %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr));
-}
-
-// Two binary32 values in one 64-bit register pair (x in the low half).
-__device__ __forceinline__ uint64_t pack_f32x2(uint32_t x, uint32_t y)
-{
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(x), "r"(y));
-    return r;
-}
-
-__device__ __forceinline__ float2 unpack_f32x2(uint64_t v)
-{
-    uint32_t x, y;
-    asm("mov.b64 {%0, %1}, %2;" : "=r"(x), "=r"(y) : "l"(v));
-    return make_float2(__uint_as_float(x), __uint_as_float(y));
-}
-
-// a * b + c on both halves, each rounded once.
-__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c)
-{
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
 
 // True in one lane of the (converged) warp.  The whole warp runs an MMA
 // issuer's loop and this picks the lane that issues: with the loop inside a
