@@ -787,47 +787,49 @@ class NestedLayerGroup:
 _DTYPES = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
 
 
-class _On:
+# The current stream's handle without the Stream object around it, where this
+# torch has it: the object costs as much host time as a kernel launch.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _same_device(device, *tensors):
+    if device.type != "cuda":
+        raise ValueError("pgf8 takes device tensors")
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"tensors on {t.device} and {device}: one call's tensors share a device")
+
+
+def _enter(device, stream):
     """Makes the device of a call's tensors and its stream current for as long
     as the call's buffers are allocated and its work enqueued, so that memory
-    that is freed on return is only reused behind that work; yields the stream's
-    handle."""
+    that is freed on return is only reused behind that work.  Returns the
+    stream's handle and what _leave takes to put the former ones back."""
+    index = device.index
+    outer = torch.cuda.current_device()
+    if stream is None:
+        if index == outer:
+            return _raw_stream(index), None
+        torch.cuda.set_device(index)
+        return _raw_stream(index), (outer, None)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=index)
+    elif stream.device.index != index:
+        raise ValueError(f"stream of {stream.device} for tensors on {device}")
+    if index != outer:
+        torch.cuda.set_device(index)
+    back = (outer, torch.cuda.current_stream())
+    torch.cuda.set_stream(stream)
+    return stream.cuda_stream, back
 
-    __slots__ = ("dev", "stream", "outer_dev", "outer_stream")
 
-    def __init__(self, device, stream, *tensors):
-        if device.type != "cuda":
-            raise ValueError("pgf8 takes device tensors")
-        for t in tensors:
-            if t is not None and t.device != device:
-                raise ValueError(f"tensors on {t.device} and {device}: one call's tensors share a device")
-        self.dev, self.stream = device.index, stream
-
-    def __enter__(self):
-        self.outer_dev = torch.cuda.current_device()
-        self.outer_stream = None
-        if self.dev != self.outer_dev:
-            torch.cuda.set_device(self.dev)
-        try:
-            if self.stream is None:
-                return torch.cuda.current_stream().cuda_stream
-            stream = self.stream
-            if not isinstance(stream, torch.cuda.Stream):
-                stream = torch.cuda.ExternalStream(int(stream), device=self.dev)
-            elif stream.device.index != self.dev:
-                raise ValueError(f"stream of {stream.device} for tensors on cuda:{self.dev}")
-            self.outer_stream = torch.cuda.current_stream()
+def _leave(back):
+    if back is not None:
+        outer, stream = back
+        if stream is not None:
             torch.cuda.set_stream(stream)
-            return stream.cuda_stream
-        except BaseException:
-            self.__exit__()
-            raise
-
-    def __exit__(self, *exc):
-        if self.outer_stream is not None:
-            torch.cuda.set_stream(self.outer_stream)
-        if self.dev != self.outer_dev:
-            torch.cuda.set_device(self.outer_dev)
+        torch.cuda.set_device(outer)
 
 
 def _code(dtype, what: str) -> int:
@@ -842,7 +844,7 @@ def _blocks(n: int) -> int:
 
 
 def _want(t: torch.Tensor, shape: tuple, dtype, what: str):
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {shape}, not {t.dtype} "
                          f"{tuple(t.shape)}")
 
@@ -854,28 +856,41 @@ def fp8_quantize_blocks(x: torch.Tensor, block_rows: int = 1, q: torch.Tensor | 
     a row (block_rows 1: activations) or per 128 x 128 block (block_rows 128:
     weights).  Returns (q uint8 of x's shape, scales f32 [.., ceil(rows /
     block_rows), ceil(cols / 128)])."""
-    if x.dim() not in (2, 3) or block_rows not in (1, 128):
+    shape = x.shape
+    dims = len(shape)
+    if dims not in (2, 3) or block_rows not in (1, 128):
         raise ValueError("x must be [rows, cols] or [batch, rows, cols], block_rows 1 or 128")
-    rows, cols = x.shape[-2:]
-    batch = x.shape[0] if x.dim() == 3 else 1
-    if cols > 1 and x.stride(-1) != 1:
+    rows, cols = shape[dims - 2], shape[dims - 1]
+    strides = x.stride()
+    if cols > 1 and strides[dims - 1] != 1:
         raise ValueError("x rows must be contiguous")
     # a dimension of one entry may carry any stride
-    ldx = x.stride(-2) if rows > 1 else max(cols, x.stride(0) if x.dim() == 3 and block_rows == 1 else 0)
-    ldb = x.stride(0) if batch > 1 else rows * ldx
+    if dims == 3:
+        batch = shape[0]
+        ldx = strides[1] if rows > 1 else max(cols, strides[0] if block_rows == 1 else 0)
+        ldb = strides[0] if batch > 1 else rows * ldx
+        sshape = (batch, -(-rows // block_rows), -(-cols // 128))
+    else:
+        batch, ldb = 1, 0
+        ldx = strides[0] if rows > 1 else cols
+        sshape = (-(-rows // block_rows), -(-cols // 128))
     code = _code(x.dtype, "x")
-    shape = (*x.shape[:-2], (rows + block_rows - 1) // block_rows, _blocks(cols))
-    with _On(x.device, stream, q, scales) as handle:
+    device = x.device
+    _same_device(device, q, scales)
+    handle, back = _enter(device, stream)
+    try:
         if q is None:
-            q = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
+            q = torch.empty(shape, dtype=torch.uint8, device=device)
         else:
-            _want(q, tuple(x.shape), torch.uint8, "q")
+            _want(q, shape, torch.uint8, "q")
         if scales is None:
-            scales = torch.empty(shape, dtype=torch.float32, device=x.device)
+            scales = torch.empty(sshape, dtype=torch.float32, device=device)
         else:
-            _want(scales, shape, torch.float32, "scales")
+            _want(scales, sshape, torch.float32, "scales")
         _check(lib.pgf8_fp8_quantize_blocks(x.data_ptr(), code, batch, rows, cols, ldx, ldb, block_rows,
                                             q.data_ptr(), scales.data_ptr(), flags, handle), "fp8_quantize_blocks")
+    finally:
+        _leave(back)
     return q, scales
 
 
@@ -888,7 +903,9 @@ def fp8_silu_mul_quantize_blocks(gu: torch.Tensor, q: torch.Tensor | None = None
         raise ValueError("gu must be [rows, 2I] with contiguous rows")
     rows, inter = gu.shape[0], gu.shape[1] // 2
     code = _code(gu.dtype, "gate/up")
-    with _On(gu.device, stream, q, scales) as handle:
+    _same_device(gu.device, q, scales)
+    handle, back = _enter(gu.device, stream)
+    try:
         if q is None:
             q = torch.empty((rows, inter), dtype=torch.uint8, device=gu.device)
         else:
@@ -900,7 +917,18 @@ def fp8_silu_mul_quantize_blocks(gu: torch.Tensor, q: torch.Tensor | None = None
         _check(lib.pgf8_fp8_silu_mul_quantize_blocks(gu.data_ptr(), code, rows, inter, _lead(gu), q.data_ptr(),
                                                      scales.data_ptr(), flags, handle),
                "fp8_silu_mul_quantize_blocks")
+    finally:
+        _leave(back)
     return q, scales
+
+
+def _workspace(t, nbytes: int, device):
+    """The given workspace, checked, or one of nbytes."""
+    if t is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device), nbytes
+    if not t.is_contiguous():
+        raise ValueError("the workspace must be contiguous")
+    return t, _nbytes(t)
 
 
 def _block_weights(wq, sw, K):
@@ -930,10 +958,14 @@ def fp8_block_linear(aq: torch.Tensor, sa: torch.Tensor, wq: torch.Tensor, sw: t
     _want(aq, (M, K), torch.uint8, "aq")
     _want(sa, (M, _blocks(K)), torch.float32, "sa")
     N = _block_weights(wq, sw, K)
-    with _On(aq.device, stream, sa, wq, sw, y) as handle:
+    _same_device(aq.device, sa, wq, sw, y)
+    handle, back = _enter(aq.device, stream)
+    try:
         y, code = _block_out(y, (M, N), out_dtype, aq.device)
         _check(lib.pgf8_fp8_block_linear(aq.data_ptr(), sa.data_ptr(), M, K, wq.data_ptr(), sw.data_ptr(), N,
                                          y.data_ptr(), code, flags, handle), "fp8_block_linear")
+    finally:
+        _leave(back)
     return y
 
 
@@ -949,14 +981,16 @@ def fp8_block_linear_dynamic(x: torch.Tensor, wq: torch.Tensor, sw: torch.Tensor
     M, K = x.shape
     xcode = _code(x.dtype, "activation")
     N = _block_weights(wq, sw, K)
-    with _On(x.device, stream, wq, sw, y, workspace) as handle:
+    _same_device(x.device, wq, sw, y, workspace)
+    handle, back = _enter(x.device, stream)
+    try:
         y, code = _block_out(y, (M, N), out_dtype, x.device)
-        if workspace is None:
-            workspace = torch.empty(lib.pgf8_fp8_block_linear_dynamic_workspace_size(M, K), dtype=torch.uint8,
-                                    device=x.device)
+        workspace, nbytes = _workspace(workspace, lib.pgf8_fp8_block_linear_dynamic_workspace_size(M, K), x.device)
         _check(lib.pgf8_fp8_block_linear_dynamic(x.data_ptr(), xcode, M, K, _lead(x) if M else K, wq.data_ptr(),
                                                  sw.data_ptr(), N, y.data_ptr(), code, workspace.data_ptr(),
-                                                 _nbytes(workspace), flags, handle), "fp8_block_linear_dynamic")
+                                                 nbytes, flags, handle), "fp8_block_linear_dynamic")
+    finally:
+        _leave(back)
     return y
 
 
@@ -1007,20 +1041,22 @@ def fp8_moe(x: torch.Tensor, w13: torch.Tensor, s13: torch.Tensor, w2: torch.Ten
     if weights is not None:
         _want(weights, (T, top_k), torch.float32, "weights")
     xcode = _code(x.dtype, "activation")
-    with _On(x.device, stream, w13, s13, w2, s2, logits, ids, weights, y, workspace) as handle:
+    _same_device(x.device, w13, s13, w2, s2, logits, ids, weights, y, workspace)
+    handle, back = _enter(x.device, stream)
+    try:
         y, ycode = _block_out(y, (T, H), out_dtype, x.device)
         if ids is None:
             ids = torch.empty((T, top_k), dtype=torch.int32, device=x.device)
         if weights is None:
             weights = torch.empty((T, top_k), dtype=torch.float32, device=x.device)
-        if workspace is None:
-            workspace = torch.empty(lib.pgf8_fp8_moe_workspace_size(T, H, F, E, top_k), dtype=torch.uint8,
-                                    device=x.device)
+        workspace, nbytes = _workspace(workspace, lib.pgf8_fp8_moe_workspace_size(T, H, F, E, top_k), x.device)
         layer = MoeLayer(x.data_ptr(), w13.data_ptr(), s13.data_ptr(), w2.data_ptr(), s2.data_ptr(),
                          None if logits is None else logits.data_ptr(), ids.data_ptr(), weights.data_ptr(),
-                         y.data_ptr(), workspace.data_ptr(), _nbytes(workspace), T, H, F, E, top_k,
+                         y.data_ptr(), workspace.data_ptr(), nbytes, T, H, F, E, top_k,
                          _lead(x) if T else H, ldl, xcode, lcode, ycode, score, 1 if renormalise else 0, factor)
         _check(lib.pgf8_fp8_moe(ctypes.byref(layer), flags, handle), "fp8_moe")
+    finally:
+        _leave(back)
     return y, ids, weights
 
 

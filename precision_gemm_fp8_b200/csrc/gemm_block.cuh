@@ -167,9 +167,7 @@ __device__ __forceinline__ uint32_t pack_out2(float2 v, int dt)
 }
 
 // Adds COLS accumulator columns of this thread's row (tensor memory at taddr)
-// times their scales (shared memory, 16-byte aligned) to acc.  Single multiply-
-// adds: the packed form (two to an instruction) needs register pairs, and the
-// moves and spills that they brought took more time than it saved.
+// times their scales (shared memory, 16-byte aligned) to acc.
 template <int COLS>
 __device__ __forceinline__ void add_scaled(uint32_t taddr, const float *sc, float (&acc)[COLS])
 {
@@ -181,10 +179,8 @@ __device__ __forceinline__ void add_scaled(uint32_t taddr, const float *sc, floa
 #pragma unroll
         for (int j = 0; j < 16; j += 4) {
             const float4 t = *reinterpret_cast<const float4 *>(sc + c0 + j);
-            acc[c0 + j] = fmaf(__uint_as_float(v[j]), t.x, acc[c0 + j]);
-            acc[c0 + j + 1] = fmaf(__uint_as_float(v[j + 1]), t.y, acc[c0 + j + 1]);
-            acc[c0 + j + 2] = fmaf(__uint_as_float(v[j + 2]), t.z, acc[c0 + j + 2]);
-            acc[c0 + j + 3] = fmaf(__uint_as_float(v[j + 3]), t.w, acc[c0 + j + 3]);
+            fma_pair(acc[c0 + j], acc[c0 + j + 1], v[j], v[j + 1], t.x, t.y);
+            fma_pair(acc[c0 + j + 2], acc[c0 + j + 3], v[j + 2], v[j + 3], t.z, t.w);
         }
     }
 }

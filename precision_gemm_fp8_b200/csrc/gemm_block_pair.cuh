@@ -14,7 +14,10 @@
 // bound by it: about 1100 cycles a k-block against the MMA's 512.  Two more
 // warps write the k-blocks' scales to a ring in shared memory: loaded by the
 // epilogue warps themselves, a row stride apart for every lane, they took more
-// of the load unit's time than the tile's multiply-adds took of theirs.
+// of the load unit's time than the tile's multiply-adds took of theirs.  The
+// additions are packed multiply-adds, two outputs to an instruction: with four
+// warps to a scheduler its issue slots are the next limit (297 us against 277
+// at 4096 x 8192 x 9472).
 //
 // Operand ring, barriers and their two-CTA signalling as in gemm_2sm.cuh: both
 // CTAs' loads complete on the even CTA's full barrier, its one MMA thread
@@ -86,7 +89,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     BlockPairCtl *ctl = reinterpret_cast<BlockPairCtl *>(smem + C::kCtlOffset);
     volatile int *abort_flag = &ctl->abort;
 
-    const int warp = threadIdx.x >> 5;
+    const int warp = warp_index();
     const int lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     const bool lead = (rank == 0);
@@ -171,8 +174,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                         }
                     }
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        acc[c + i] = fmaf(__uint_as_float(v[i]), f, acc[c + i]);
+                    for (int i = 0; i < 16; i += 2)
+                        fma_pair(acc[c + i], acc[c + i + 1], v[i], v[i + 1], f, f);
                 }
             }
             if (!ok)

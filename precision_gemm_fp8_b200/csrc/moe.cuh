@@ -1,8 +1,8 @@
 // A mixture-of-experts layer for a few tokens (T <= 64), E4M3 weights with
 // 128 x 128 block scales, in three launches:
-//   moe_plan_kernel     routing (top-k of the logits) and the list of the chosen
-//                       experts' tokens by one CTA; the others quantise x per
-//                       1 x 128 group
+//   moe_plan_kernel     routing (top-k of the logits) by a cluster of up to eight
+//                       CTAs, whose first then lists the chosen experts' tokens;
+//                       the other CTAs quantise x per 1 x 128 group
 //   moe_gate_up_kernel  for every chosen expert and 128 hidden features:
 //                       g = xq W1, u = xq W3, h = silu(g) u in binary32, E4M3
 //                       codes of h with one scale per 1 x 128 group
@@ -33,7 +33,7 @@ namespace pgf8 {
 constexpr int kMoeMaxTokens = 64;     // one 64-bit mask of tokens per expert
 constexpr int kMoeMaxExperts = 512;   // 16 logits a lane
 constexpr int kMoeMaxTopK = 16;
-constexpr int kMoePlanThreads = 1024; // one thread per (token, choice) pair
+constexpr int kMoePlanThreads = 256;  // of each CTA: eight tokens to route, or 32 groups to quantise
 
 enum : int { kMoeSoftmax = 0, kMoeSigmoid = 1 };
 
@@ -52,43 +52,65 @@ struct MoeRouteParams {
     uint8_t *xq;           // [T, H]
     float *sx;             // [T, hblocks]
     const void *logits;    // [T, E], row stride ldl; null: ids / weights are given
+    int ldt;               // pgf8_dtype of logits
     int64_t ldl;
     int E, K;              // K choices a token
     int score, renorm;
     float factor;
     int *ids;              // [T, K]; written with logits (may then be null), read without
     float *weights;        // [T, K]
+    int route_ctas;        // CTAs of a cluster: 1, 2, 4 or 8
     MoePlan plan;
 };
 
-__device__ __forceinline__ float to_float(float v) { return v; }
-__device__ __forceinline__ float to_float(__half v) { return __half2float(v); }
-__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+// Largest logits first: an order-preserving 32-bit key of v (-0 as +0, which are ties).
+__device__ __forceinline__ uint32_t logit_key(float v)
+{
+    const uint32_t u = __float_as_uint(v + 0.0f);
+    return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+}
+
+__device__ __forceinline__ void st_shared_cluster_u32(uint32_t addr, uint32_t v)
+{
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
 
 // One warp routes one token: the K largest logits (ties to the lowest index;
 // NaN and -inf are never chosen: id -1, weight 0), their softmax over all E or
-// their sigmoids, divided by their sum if asked, times factor.
-template <typename L>
-__device__ __forceinline__ void route_token(const MoeRouteParams &p, int t, int *sid, float *sw)
+// their sigmoids, divided by their sum if asked, times factor.  PER logits a
+// lane (E <= 32 PER).  Each choice is two warp reductions in hardware: the
+// largest key, then the lowest index that has it.  The choices go to sid / sw
+// in the shared memory of the cluster's first CTA.
+template <int PER>
+__device__ __forceinline__ void route_token(const MoeRouteParams &p, int t, uint32_t sid, uint32_t sw)
 {
-    constexpr int PER = kMoeMaxExperts / 32;
     const int lane = threadIdx.x & 31;
     const float ninf = -INFINITY;
-    const L *row = static_cast<const L *>(p.logits) + static_cast<int64_t>(t) * p.ldl;
+    const int64_t row = static_cast<int64_t>(t) * p.ldl;
     float v[PER];
+    uint32_t key[PER];   // 0 for a logit that cannot be chosen
     float top = ninf;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         const int e = lane + 32 * i;
-        float f = e < p.E ? to_float(row[e]) : ninf;
+        float f = ninf;
+        if (e < p.E) {
+            if (p.ldt == 0)
+                f = static_cast<const float *>(p.logits)[row + e];
+            else if (p.ldt == 1)
+                f = __half2float(static_cast<const __half *>(p.logits)[row + e]);
+            else
+                f = __bfloat162float(static_cast<const __nv_bfloat16 *>(p.logits)[row + e]);
+        }
         v[i] = f != f ? ninf : f;
+        key[i] = v[i] > ninf ? logit_key(v[i]) : 0u;
         top = fmaxf(top, v[i]);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     float sum = 0.0f;
-    if (p.score == kMoeSoftmax && top > ninf) {
+    if (p.score == kMoeSoftmax) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
 #pragma unroll
         for (int i = 0; i < PER; ++i)
             sum += v[i] > ninf ? expf(v[i] - top) : 0.0f;
@@ -96,55 +118,56 @@ __device__ __forceinline__ void route_token(const MoeRouteParams &p, int t, int 
         for (int o = 16; o > 0; o >>= 1)
             sum += __shfl_xor_sync(0xffffffffu, sum, o);
     }
-    unsigned taken = 0;
-    float mine = 0.0f, chosen_sum = 0.0f;   // lane j keeps choice j
+    uint32_t my_key = 0u;   // lane j keeps choice j
     int my_id = -1;
     for (int j = 0; j < p.K; ++j) {
-        float best = ninf;
+        uint32_t best = 0u;
         int at = 0x7FFFFFFF;
 #pragma unroll
         for (int i = 0; i < PER; ++i)
-            if (!((taken >> i) & 1u) && v[i] > best) {
-                best = v[i];
+            if (key[i] > best) {
+                best = key[i];
                 at = lane + 32 * i;
             }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            const float ob = __shfl_xor_sync(0xffffffffu, best, o);
-            const int oa = __shfl_xor_sync(0xffffffffu, at, o);
-            if (ob > best || (ob == best && oa < at)) {
-                best = ob;
-                at = oa;
-            }
-        }
-        if (best == ninf)
+        const uint32_t most = __reduce_max_sync(0xffffffffu, best);
+        if (most == 0u)
             break;   // nothing left to choose (the same in every lane)
-        if ((at & 31) == lane)
-            taken |= 1u << (at >> 5);
-        const float w = p.score == kMoeSoftmax ? __fdiv_rn(expf(best - top), sum)
-                                               : __fdiv_rn(1.0f, 1.0f + expf(-best));
-        chosen_sum += w;
+        const int id = static_cast<int>(
+            __reduce_min_sync(0xffffffffu, best == most ? static_cast<unsigned>(at) : 0x7FFFFFFFu));
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (id == lane + 32 * i)
+                key[i] = 0u;
         if (lane == j) {
-            mine = w;
-            my_id = at;
+            my_key = most;
+            my_id = id;
         }
     }
+    float mine = 0.0f;
+    if (my_id >= 0) {
+        const float f = __uint_as_float((my_key & 0x80000000u) ? my_key & 0x7FFFFFFFu : ~my_key);
+        mine = p.score == kMoeSoftmax ? __fdiv_rn(expf(f - top), sum) : __fdiv_rn(1.0f, 1.0f + expf(-f));
+    }
+    if (p.renorm) {
+        float all = mine;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            all += __shfl_xor_sync(0xffffffffu, all, o);
+        mine = all != 0.0f ? __fdiv_rn(mine, all) : 0.0f;
+    }
+    mine = my_id >= 0 ? mine * p.factor : 0.0f;
     if (lane < p.K) {
-        if (p.renorm)
-            mine = chosen_sum != 0.0f ? __fdiv_rn(mine, chosen_sum) : 0.0f;
-        mine *= p.factor;
-        if (my_id < 0)
-            mine = 0.0f;
-        sid[t * p.K + lane] = my_id;
-        sw[t * p.K + lane] = mine;
+        const int at = t * p.K + lane;
+        st_shared_cluster_u32(sid + at * 4, static_cast<uint32_t>(my_id));
+        st_shared_cluster_u32(sw + at * 4, __float_as_uint(mine));
         if (p.ids)
-            p.ids[t * p.K + lane] = my_id;
+            p.ids[at] = my_id;
         if (p.weights)
-            p.weights[t * p.K + lane] = mine;
+            p.weights[at] = mine;
     }
 }
 
-// Inclusive sum over the CTA's kMoePlanThreads threads (red: 32 ints).
+// Inclusive sum over the CTA's kMoePlanThreads threads (red: one int a warp).
 __device__ __forceinline__ int plan_scan(int v, int *red)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -157,47 +180,38 @@ __device__ __forceinline__ int plan_scan(int v, int *red)
     if (lane == 31)
         red[warp] = v;
     __syncthreads();
-    if (warp == 0) {
-        int w = red[lane];
+    int before = 0;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(0xffffffffu, w, o);
-            if (lane >= o)
-                w += u;
-        }
-        red[lane] = w;
-    }
-    __syncthreads();
-    const int r = v + (warp > 0 ? red[warp - 1] : 0);
-    __syncthreads();   // red may be written again
-    return r;
+    for (int w = 0; w < kMoePlanThreads / 32; ++w)
+        before += w < warp ? red[w] : 0;
+    return v + before;
 }
 
-// Block 0 routes and plans; the others quantise x, 128 groups each.
-template <typename T, typename L>
-__global__ void __launch_bounds__(kMoePlanThreads) moe_plan_kernel(const MoeRouteParams p)
+// Cluster 0 routes (eight tokens to a CTA) and its first CTA plans; the other
+// clusters' CTAs quantise x, 32 groups each.
+template <typename T> __global__ void __launch_bounds__(kMoePlanThreads) moe_plan_kernel(const MoeRouteParams p)
 {
+    static_assert(kMoeMaxExperts == 2 * kMoePlanThreads, "two experts a thread");
+    const bool routes = static_cast<int>(blockIdx.x) < p.route_ctas;
+    if (routes && p.route_ctas > 1)
+        cluster_arrive_relaxed();   // this CTA runs: the others may write to its shared memory
     grid_launch_dependents();
     grid_dependency_wait();
     const int tid = threadIdx.x;
-    if (blockIdx.x > 0) {
-        const int g = (static_cast<int>(blockIdx.x) - 1) * (kMoePlanThreads / 8) + (tid >> 3);
+    if (!routes) {
+        const int g = (static_cast<int>(blockIdx.x) - p.route_ctas) * (kMoePlanThreads / 8) + (tid >> 3);
         const int row = g / p.hblocks, grp = g - row * p.hblocks;
         const int c = grp * 128 + (tid & 7) * 16;
         const bool live = row < p.T && c < p.H;
         Vec16<T> v;
-        float a = 0.0f;
-        if (live) {
+        if (live)
             v.load(static_cast<const T *>(p.x) + static_cast<int64_t>(row) * p.ldx + c);
-            a = amax16(v.v);
-        }
-        a = group_max8(a);
+        const GroupScale g8(v.v, live);
         if (!live)
             return;
-        const float s = block_scale(a);
-        *reinterpret_cast<uint4 *>(p.xq + static_cast<int64_t>(row) * p.H + c) = encode16(v.v, RowDivisor(s));
+        *reinterpret_cast<uint4 *>(p.xq + static_cast<int64_t>(row) * p.H + c) = g8.encode(v.v);
         if ((tid & 7) == 0)
-            p.sx[row * p.hblocks + grp] = s;
+            p.sx[row * p.hblocks + grp] = g8.d.s;
         return;
     }
 
@@ -205,44 +219,75 @@ __global__ void __launch_bounds__(kMoePlanThreads) moe_plan_kernel(const MoeRout
     __shared__ float sw[kMoeMaxTokens * kMoeMaxTopK];
     __shared__ unsigned mask[kMoeMaxExperts][2];   // tokens of each expert
     __shared__ int first[kMoeMaxExperts];          // its first row
-    __shared__ int red[32];
+    __shared__ int red[kMoePlanThreads / 32];
     const int pairs = p.T * p.K;
-    if (tid < kMoeMaxExperts)
-        mask[tid][0] = mask[tid][1] = 0u;
+    for (int e = tid; e < kMoeMaxExperts; e += kMoePlanThreads)
+        mask[e][0] = mask[e][1] = 0u;
+    if (p.route_ctas > 1)
+        cluster_wait_acquire();
     if (p.logits) {
-        for (int t = tid >> 5; t < p.T; t += kMoePlanThreads / 32)
-            route_token<L>(p, t, sid, sw);
-    } else if (tid < pairs) {
-        sid[tid] = p.ids[tid];
-        sw[tid] = p.weights[tid];
+        const int t = static_cast<int>(blockIdx.x) * (kMoePlanThreads / 32) + (tid >> 5);
+        if (t < p.T) {
+            const uint32_t id0 = map_shared_rank(smem_u32(sid), 0), w0 = map_shared_rank(smem_u32(sw), 0);
+            if (p.E <= 64)
+                route_token<2>(p, t, id0, w0);
+            else if (p.E <= 128)
+                route_token<4>(p, t, id0, w0);
+            else if (p.E <= 256)
+                route_token<8>(p, t, id0, w0);
+            else
+                route_token<16>(p, t, id0, w0);
+        }
+        __syncwarp();
+        if (p.route_ctas > 1) {
+            cluster_sync_all();
+            if (blockIdx.x > 0)
+                return;
+        }
+    } else {
+        for (int i = tid; i < pairs; i += kMoePlanThreads) {
+            sid[i] = p.ids[i];
+            sw[i] = p.weights[i];
+        }
     }
     __syncthreads();
-    const int t = tid / p.K;
-    const int e = tid < pairs ? sid[tid] : -1;
-    const bool chosen = e >= 0 && e < p.E;
-    if (chosen)
-        atomicOr(&mask[e][t >> 5], 1u << (t & 31));
+    auto expert = [&](int i) {   // of pair i, -1 for a slot that is left out
+        const int e = sid[i];
+        return e >= 0 && e < p.E ? e : -1;
+    };
+    for (int i = tid; i < pairs; i += kMoePlanThreads) {
+        const int e = expert(i), t = i / p.K;
+        if (e >= 0)
+            atomicOr(&mask[e][t >> 5], 1u << (t & 31));
+    }
     __syncthreads();
-    const int rows = tid < p.E ? __popc(mask[tid][0]) + __popc(mask[tid][1]) : 0;
+    const int e0 = 2 * tid;
+    const int rows0 = __popc(mask[e0][0]) + __popc(mask[e0][1]);
+    const int rows1 = __popc(mask[e0 + 1][0]) + __popc(mask[e0 + 1][1]);
     // both sums in one scan: rows (at most 1024) above the count of experts (at most 512)
-    const int both = plan_scan((rows << 16) | (rows > 0 ? 1 : 0), red);
-    if (tid < p.E) {
-        const int row0 = (both >> 16) - rows;
-        first[tid] = row0;
-        if (rows > 0)
-            p.plan.experts[(both & 0xFFFF) - 1] = make_int4(tid, row0, rows, 0);
-    }
+    const int mine = ((rows0 + rows1) << 16) | ((rows0 > 0) + (rows1 > 0));
+    const int both = plan_scan(mine, red), before = both - mine;
+    first[e0] = before >> 16;
+    first[e0 + 1] = (before >> 16) + rows0;
+    int n = before & 0xFFFF;
+    if (rows0 > 0)
+        p.plan.experts[n++] = make_int4(e0, first[e0], rows0, 0);
+    if (rows1 > 0)
+        p.plan.experts[n] = make_int4(e0 + 1, first[e0 + 1], rows1, 0);
     if (tid == kMoePlanThreads - 1)
         *p.plan.active = both & 0xFFFF;
     __syncthreads();
-    if (chosen) {
+    for (int i = tid; i < pairs; i += kMoePlanThreads) {
+        const int e = expert(i);
+        if (e < 0)
+            continue;
         // a token that names an expert twice is one row with both weights
-        const int j0 = t * p.K;
+        const int t = i / p.K;
         float w = 0.0f;
         bool again = false;
-        for (int j = j0; j < j0 + p.K; ++j)
+        for (int j = t * p.K; j < (t + 1) * p.K; ++j)
             if (sid[j] == e) {
-                again = again || j < tid;
+                again = again || j < i;
                 w += sw[j];
             }
         if (!again) {
@@ -304,23 +349,16 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS)
     BlockCtl *ctl = reinterpret_cast<BlockCtl *>(smem + C::kCtlOffset);
     volatile int *abort_flag = &ctl->abort;
 
-    const int warp = threadIdx.x >> 5;
+    const int warp = warp_index();
     const int lane = threadIdx.x & 31;
     const int f0 = static_cast<int>(blockIdx.x) * 128;
     const int splits = static_cast<int>(gridDim.z);
     const int kb0 = static_cast<int>(static_cast<int64_t>(p.hblocks) * blockIdx.z / splits);
     const int kb1 = static_cast<int>(static_cast<int64_t>(p.hblocks) * (blockIdx.z + 1) / splits);
 
-    // The plan comes from the kernel before.  Dependents (the down kernel) may
-    // start once every CTA of this grid is past its wait: the plan is complete
-    // then, and they read it, and weights, before this grid has finished.
-    grid_dependency_wait();
-    grid_launch_dependents();
-    if (static_cast<int>(blockIdx.y) >= __ldcg(p.plan.active))
-        return;   // the whole cluster
-    const int4 ex = __ldcg(p.plan.experts + blockIdx.y);
-
     if (threadIdx.x == 0) {
+        tma_prefetch_desc(&tmX);
+        tma_prefetch_desc(&tmW);
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(&ctl->full[s], 1);
             mbar_init(&ctl->empty[s], 1);
@@ -341,6 +379,19 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = ctl->tmem_base;
+
+    // The plan comes from the kernel before.  Dependents (the down kernel) may
+    // start once every CTA of this grid is past its wait: the plan is complete
+    // then, and they read it, and weights, before this grid has finished.
+    grid_dependency_wait();
+    grid_launch_dependents();
+    if (static_cast<int>(blockIdx.y) >= __ldcg(p.plan.active)) {
+        // the whole cluster; nothing of it is in flight
+        if (warp == 1)
+            tmem_dealloc(tmem, C::kTmemCols);
+        return;
+    }
+    const int4 ex = __ldcg(p.plan.experts + blockIdx.y);
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
@@ -600,7 +651,7 @@ __global__ void __launch_bounds__(C::kThreads)
     float *weight = reinterpret_cast<float *>(tok + p.pairs);
     volatile int *abort_flag = &ctl->abort;
 
-    const int warp = threadIdx.x >> 5;
+    const int warp = warp_index();
     const int lane = threadIdx.x & 31;
     const int splits = static_cast<int>(gridDim.z);
 

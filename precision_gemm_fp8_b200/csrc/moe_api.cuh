@@ -176,6 +176,7 @@ pgf8_status pgf8_fp8_moe(const pgf8_fp8_moe_layer *layer, int32_t flags, void *s
     r.xq = base + ws.xq;
     r.sx = f32(ws.sx);
     r.logits = a.logits;
+    r.ldt = a.ldt;
     r.ldl = a.ldl;
     r.E = E;
     r.K = K;
@@ -185,14 +186,24 @@ pgf8_status pgf8_fp8_moe(const pgf8_fp8_moe_layer *layer, int32_t flags, void *s
     r.ids = a.ids;
     r.weights = a.weights;
     r.plan = plan;
-    const unsigned grid = 1 + static_cast<unsigned>((static_cast<int64_t>(T) * hblocks + 127) / 128);
+    // eight tokens to a routing CTA, the CTAs of one cluster; whole clusters of 32-group CTAs for x
+    int route = 1;
+    while (a.logits && route * (kMoePlanThreads / 32) < T)
+        route *= 2;
+    r.route_ctas = route;
+    const int64_t quant = ceil_div(static_cast<int64_t>(T) * hblocks, kMoePlanThreads / 8);
+    const unsigned grid = static_cast<unsigned>(route + ceil_div(quant, route) * route);
     st = by_dtype(a.xdt, [&](auto *x) {
         using X = std::remove_cv_t<std::remove_pointer_t<decltype(x)>>;
-        return by_dtype(a.logits ? a.ldt : PGF8_F32, [&](auto *l) {
-            using L = std::remove_cv_t<std::remove_pointer_t<decltype(l)>>;
-            return launch_grid(moe_plan_kernel<X, L>, dim3(grid), dim3(kMoePlanThreads), cs,
-                               (flags & PGF8_FLAG_OVERLAP_PREVIOUS) ? 1 : 0, r);
-        });
+        cudaLaunchConfig_t cfg;
+        std::memset(&cfg, 0, sizeof(cfg));
+        cfg.gridDim = dim3(grid, 1, 1);
+        cfg.blockDim = dim3(kMoePlanThreads, 1, 1);
+        cfg.stream = cs;
+        cudaLaunchAttribute attrs[2];
+        fill_attrs(cfg, attrs, 1, (flags & PGF8_FLAG_OVERLAP_PREVIOUS) ? 1 : 0, route);
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, moe_plan_kernel<X>, r);
+        return e == cudaSuccess ? PGF8_OK : cuda_fail(e);
     });
     if (st != PGF8_OK)
         return st;
