@@ -880,11 +880,11 @@ def fp8_quantize_blocks(x: torch.Tensor, block_rows: int = 1, q: torch.Tensor | 
     handle, back = _enter(device, stream)
     try:
         if q is None:
-            q = torch.empty(shape, dtype=torch.uint8, device=device)
+            q = x.new_empty(shape, dtype=torch.uint8)
         else:
             _want(q, shape, torch.uint8, "q")
         if scales is None:
-            scales = torch.empty(sshape, dtype=torch.float32, device=device)
+            scales = x.new_empty(sshape, dtype=torch.float32)
         else:
             _want(scales, sshape, torch.float32, "scales")
         _check(lib.pgf8_fp8_quantize_blocks(x.data_ptr(), code, batch, rows, cols, ldx, ldb, block_rows,
@@ -907,11 +907,11 @@ def fp8_silu_mul_quantize_blocks(gu: torch.Tensor, q: torch.Tensor | None = None
     handle, back = _enter(gu.device, stream)
     try:
         if q is None:
-            q = torch.empty((rows, inter), dtype=torch.uint8, device=gu.device)
+            q = gu.new_empty((rows, inter), dtype=torch.uint8)
         else:
             _want(q, (rows, inter), torch.uint8, "q")
         if scales is None:
-            scales = torch.empty((rows, _blocks(inter)), dtype=torch.float32, device=gu.device)
+            scales = gu.new_empty((rows, _blocks(inter)), dtype=torch.float32)
         else:
             _want(scales, (rows, _blocks(inter)), torch.float32, "scales")
         _check(lib.pgf8_fp8_silu_mul_quantize_blocks(gu.data_ptr(), code, rows, inter, _lead(gu), q.data_ptr(),
@@ -922,26 +922,27 @@ def fp8_silu_mul_quantize_blocks(gu: torch.Tensor, q: torch.Tensor | None = None
     return q, scales
 
 
-def _workspace(t, nbytes: int, device):
-    """The given workspace, checked, or one of nbytes."""
+def _workspace(t, nbytes: int, like):
+    """The given workspace, checked, or one of nbytes where `like` is."""
     if t is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device), nbytes
+        return like.new_empty(nbytes, dtype=torch.uint8), nbytes
     if not t.is_contiguous():
         raise ValueError("the workspace must be contiguous")
     return t, _nbytes(t)
 
 
 def _block_weights(wq, sw, K):
-    if wq.dim() != 2 or wq.shape[1] != K:
+    shape = wq.shape
+    if len(shape) != 2 or shape[1] != K:
         raise ValueError(f"wq must be [N, {K}]")
-    _want(wq, tuple(wq.shape), torch.uint8, "wq")
-    _want(sw, (_blocks(wq.shape[0]), _blocks(K)), torch.float32, "sw")
-    return wq.shape[0]
+    _want(wq, shape, torch.uint8, "wq")
+    _want(sw, (-(-shape[0] // 128), -(-K // 128)), torch.float32, "sw")
+    return shape[0]
 
 
-def _block_out(y, shape, out_dtype, device):
+def _block_out(y, shape, out_dtype, like):
     if y is None:
-        return torch.empty(shape, dtype=out_dtype, device=device), _code(out_dtype, "output")
+        return like.new_empty(shape, dtype=out_dtype), _code(out_dtype, "output")
     _want(y, shape, y.dtype, "y")
     return y, _code(y.dtype, "output")
 
@@ -961,7 +962,7 @@ def fp8_block_linear(aq: torch.Tensor, sa: torch.Tensor, wq: torch.Tensor, sw: t
     _same_device(aq.device, sa, wq, sw, y)
     handle, back = _enter(aq.device, stream)
     try:
-        y, code = _block_out(y, (M, N), out_dtype, aq.device)
+        y, code = _block_out(y, (M, N), out_dtype, aq)
         _check(lib.pgf8_fp8_block_linear(aq.data_ptr(), sa.data_ptr(), M, K, wq.data_ptr(), sw.data_ptr(), N,
                                          y.data_ptr(), code, flags, handle), "fp8_block_linear")
     finally:
@@ -984,8 +985,8 @@ def fp8_block_linear_dynamic(x: torch.Tensor, wq: torch.Tensor, sw: torch.Tensor
     _same_device(x.device, wq, sw, y, workspace)
     handle, back = _enter(x.device, stream)
     try:
-        y, code = _block_out(y, (M, N), out_dtype, x.device)
-        workspace, nbytes = _workspace(workspace, lib.pgf8_fp8_block_linear_dynamic_workspace_size(M, K), x.device)
+        y, code = _block_out(y, (M, N), out_dtype, x)
+        workspace, nbytes = _workspace(workspace, lib.pgf8_fp8_block_linear_dynamic_workspace_size(M, K), x)
         _check(lib.pgf8_fp8_block_linear_dynamic(x.data_ptr(), xcode, M, K, _lead(x) if M else K, wq.data_ptr(),
                                                  sw.data_ptr(), N, y.data_ptr(), code, workspace.data_ptr(),
                                                  nbytes, flags, handle), "fp8_block_linear_dynamic")
@@ -1020,7 +1021,8 @@ def fp8_moe(x: torch.Tensor, w13: torch.Tensor, s13: torch.Tensor, w2: torch.Ten
     T, H = x.shape
     if w13.dim() != 3 or w13.shape[1] % 2:
         raise ValueError("w13 must be [E, 2F, H]")
-    E, F = w13.shape[0], w13.shape[1] // 2
+    E, F = w13.shape[:2]
+    F //= 2
     _want(w13, (E, 2 * F, H), torch.uint8, "w13")
     _want(s13, (E, 2, _blocks(F), _blocks(H)), torch.float32, "s13")
     _want(w2, (E, H, F), torch.uint8, "w2")
@@ -1028,7 +1030,7 @@ def fp8_moe(x: torch.Tensor, w13: torch.Tensor, s13: torch.Tensor, w2: torch.Ten
     if logits is not None:
         if top_k is None:
             raise ValueError("routing from logits needs top_k")
-        if tuple(logits.shape) != (T, E) or (E > 1 and logits.stride(1) != 1):
+        if logits.shape != (T, E) or (E > 1 and logits.stride(1) != 1):
             raise ValueError(f"logits must be [{T}, {E}] with contiguous rows")
         lcode, ldl = _code(logits.dtype, "logits"), _lead(logits) if T else E
     else:
@@ -1044,12 +1046,12 @@ def fp8_moe(x: torch.Tensor, w13: torch.Tensor, s13: torch.Tensor, w2: torch.Ten
     _same_device(x.device, w13, s13, w2, s2, logits, ids, weights, y, workspace)
     handle, back = _enter(x.device, stream)
     try:
-        y, ycode = _block_out(y, (T, H), out_dtype, x.device)
+        y, ycode = _block_out(y, (T, H), out_dtype, x)
         if ids is None:
-            ids = torch.empty((T, top_k), dtype=torch.int32, device=x.device)
+            ids = x.new_empty((T, top_k), dtype=torch.int32)
         if weights is None:
-            weights = torch.empty((T, top_k), dtype=torch.float32, device=x.device)
-        workspace, nbytes = _workspace(workspace, lib.pgf8_fp8_moe_workspace_size(T, H, F, E, top_k), x.device)
+            weights = x.new_empty((T, top_k), dtype=torch.float32)
+        workspace, nbytes = _workspace(workspace, lib.pgf8_fp8_moe_workspace_size(T, H, F, E, top_k), x)
         layer = MoeLayer(x.data_ptr(), w13.data_ptr(), s13.data_ptr(), w2.data_ptr(), s2.data_ptr(),
                          None if logits is None else logits.data_ptr(), ids.data_ptr(), weights.data_ptr(),
                          y.data_ptr(), workspace.data_ptr(), nbytes, T, H, F, E, top_k,

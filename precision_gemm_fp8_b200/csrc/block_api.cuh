@@ -79,18 +79,91 @@ struct BlockLaunch {
     cudaStream_t stream;
 };
 
-// K-split of the weight-streaming kernels: the largest cluster that keeps the
-// grid within `slots` CTAs, all of them resident at once with SMs to spare
-// (one token, 12288 x 4096, 96 tiles: 12.9 us at 2, 16.3 at 3 with 288 of 296
-// places taken, 13.9 at 1; 64 tiles of 8192 x 28672: 38.4 at 4, 44.0 at 6), and
-// leaves at least four k-blocks to a CTA.
-static int block_splits(int64_t tiles, int64_t kblocks, int64_t slots)
+// ------------------------------------------------------------------ kernel choice
+// How many clusters of each size the current device holds at once, for one
+// kernel at one amount of shared memory (a cluster's CTAs share a GPC, so
+// this is less than the CTAs that fit divided by the size: 16 clusters of 8
+// CTAs at one to an SM do not all run at once on a B200, and a grid that
+// counts on it takes two rounds).  For kernels that allocate tensor memory the
+// occupancy query answers for one CTA to an SM; where two fit (per_sm), a
+// cluster takes half as many SMs (measured: 32 clusters of 8 and 80 of 3 run in
+// one round, 96 of 3 and 64 of 6 do not).  Set up once per device.
+constexpr int kMaxCluster = 8;
+
+struct ClusterFit {
+    PerDeviceSetup setup;
+    int fit[kSetupDevices + 1][kMaxCluster + 1];
+};
+
+template <typename... Args>
+static cudaError_t cluster_fit(ClusterFit &c, void (*kernel)(Args...), int threads, int attr_smem, int smem,
+                               int per_sm, const int *&fit)
 {
-    static const int kSizes[] = {8, 6, 4, 3, 2};
-    for (int s : kSizes)
-        if (tiles * s <= slots && kblocks >= 4 * s)
-            return s;
-    return 1;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    int *row = c.fit[dev >= 0 && dev < kSetupDevices ? dev : kSetupDevices];
+    e = setup_once_per_device(c.setup, [=](int, int *) {
+        cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, attr_smem);
+        if (err == cudaSuccess)
+            err = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                       cudaSharedmemCarveoutMaxShared);
+        for (int s = 1; s <= kMaxCluster && err == cudaSuccess; ++s) {
+            cudaLaunchConfig_t q;
+            std::memset(&q, 0, sizeof(q));
+            q.gridDim = dim3(1, 1, static_cast<unsigned>(s));
+            q.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+            q.dynamicSmemBytes = static_cast<size_t>(smem);
+            cudaLaunchAttribute qa[2];
+            qa[0].id = cudaLaunchAttributeClusterDimension;
+            qa[0].val.clusterDim.x = qa[0].val.clusterDim.y = 1;
+            qa[0].val.clusterDim.z = static_cast<unsigned>(s);
+            q.attrs = qa;
+            q.numAttrs = 1;
+            int n = 0;
+            err = cudaOccupancyMaxActiveClusters(&n, kernel, &q);
+            row[s] = n > 0 ? n : 1;
+        }
+        if (per_sm >= 2)
+            for (int s = kMaxCluster; s >= 1; --s)
+                row[s] = s % 2 == 0 ? row[s / 2] : 2 * row[s];
+        return err;
+    });
+    fit = row;
+    return e;
+}
+
+// Estimated time in us, measured on a B200 (fixed part about 4 us for every
+// kernel, so that it cancels), and the K-split that gives it.
+struct BlockPlan {
+    double us;
+    int splits;
+};
+
+// A weight-streaming kernel over `tiles` weight tiles of `kblocks` k-blocks,
+// `kb_us` a k-block for one SM: the longest of its rounds' k-blocks one after
+// another, of the SMs' total work, and of the weights at HBM speed; 0.7 us for
+// the exchange of a split sum, 2 us for each further round, and a quarter of a
+// CTA's own k-blocks, by which they end apart.  One token (us at splits of 1, 2,
+// 3, 4, 6, 8): 4096 x 4096 12.7, 8.9, 8.0, 7.4, 7.6, 6.3; 12288 x 4096 13.9, 12.9,
+// 16.3, 15.4, 18.5, 17.8; 8192 x 28672 72.5, 41.7, 39.9, 38.4, 44.0, 41.5.
+static BlockPlan stream_plan(int64_t tiles, int64_t kblocks, double kb_us, double weight_bytes, const int *fit)
+{
+    static const int kSizes[] = {1, 2, 3, 4, 6, 8};
+    BlockPlan best = {1e30, 1};
+    const int sms = num_sms();
+    for (int s : kSizes) {
+        if (s > 1 && kblocks < 2 * s)
+            break;
+        const double rounds = static_cast<double>(ceil_div(tiles, fit[s]));
+        const double own = static_cast<double>(ceil_div(kblocks, s)) * kb_us;
+        double us = std::fmax(rounds * own, static_cast<double>(tiles) * kblocks * kb_us / sms);
+        us = std::fmax(us, weight_bytes / 6.2e6) + 0.25 * own + 2.0 * (rounds - 1.0) + (s > 1 ? 0.7 : 0.0);
+        if (us < best.us)
+            best = {us, s};
+    }
+    return best;
 }
 
 static BlockParams block_params(const BlockLaunch &L)
@@ -108,9 +181,6 @@ static BlockParams block_params(const BlockLaunch &L)
     return p;
 }
 
-// CTAs that the grid of a weight-streaming kernel may have, at one or two to an SM.
-static int64_t block_slots(int ctas_per_sm) { return ctas_per_sm == 1 ? num_sms() : num_sms() * 7 / 4; }
-
 template <class C> static bool block_maps(const BlockLaunch &L, CUtensorMap &tmX, CUtensorMap &tmW)
 {
     return make_map(&tmX, L.aq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, L.M, L.K, 128, C::kRowsX,
@@ -119,36 +189,43 @@ template <class C> static bool block_maps(const BlockLaunch &L, CUtensorMap &tmX
                     CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <class C> static pgf8_status launch_block(const BlockLaunch &L, int ctas_per_sm)
+template <class C> static cudaError_t block_fit(const int *&fit)
 {
-    static PerDeviceSetup setup;
-    const cudaError_t attr_err = setup_once_per_device(setup, [](int, int *) {
-        cudaError_t e = cudaFuncSetAttribute(gemm_block_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             C::kSmemBytes);
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(gemm_block_kernel<C>, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                     cudaSharedmemCarveoutMaxShared);
-        return e;
-    });
-    if (attr_err != cudaSuccess)
-        return cuda_fail(attr_err);
+    static ClusterFit c;
+    return cluster_fit(c, gemm_block_kernel<C>, C::kThreads, C::kSmemBytes, C::kSmemBytes, C::CTAS, fit);
+}
+
+// kb_us: see stream_plan.
+template <class C> static BlockPlan plan_block(const BlockLaunch &L, double kb_us)
+{
+    const int *fit = nullptr;
+    if (block_fit<C>(fit) != cudaSuccess)
+        return {1e29, 1};
+    const int64_t nt = ceil_div(L.N, 128), mt = ceil_div(L.M, C::BN);
+    if (mt > 65535)   // the grid's y extent
+        return {1e30, 1};
+    return stream_plan(nt * mt, ceil_div(L.K, 128), kb_us, static_cast<double>(L.N) * L.K, fit);
+}
+
+template <class C> static pgf8_status launch_block(const BlockLaunch &L, int splits)
+{
+    const int *fit = nullptr;
+    cudaError_t e = block_fit<C>(fit);
+    if (e != cudaSuccess)
+        return cuda_fail(e);
     CUtensorMap tmX, tmW;
     if (!block_maps<C>(L, tmX, tmW))
         return PGF8_ERR_UNSUPPORTED;
-    const BlockParams p = block_params(L);
-    const int64_t nt = ceil_div(L.N, 128), mt = ceil_div(L.M, C::BN);
-    if (mt > 65535)
-        return PGF8_ERR_UNSUPPORTED;   // the grid's y extent
-    const int splits = block_splits(nt * mt, p.kblocks, block_slots(ctas_per_sm));
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof(cfg));
-    cfg.gridDim = dim3(static_cast<unsigned>(nt), static_cast<unsigned>(mt), static_cast<unsigned>(splits));
+    cfg.gridDim = dim3(static_cast<unsigned>(ceil_div(L.N, 128)), static_cast<unsigned>(ceil_div(L.M, C::BN)),
+                       static_cast<unsigned>(splits));
     cfg.blockDim = dim3(C::kThreads, 1, 1);
     cfg.dynamicSmemBytes = C::kSmemBytes;
     cfg.stream = L.stream;
     cudaLaunchAttribute attrs[2];
     fill_attrs(cfg, attrs, splits, 1);
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, gemm_block_kernel<C>, tmX, tmW, p);
+    e = cudaLaunchKernelEx(&cfg, gemm_block_kernel<C>, tmX, tmW, block_params(L));
     return e == cudaSuccess ? PGF8_OK : cuda_fail(e);
 }
 
@@ -194,25 +271,33 @@ template <class C> static pgf8_status launch_block_pair(const BlockLaunch &L)
     return e == cudaSuccess ? PGF8_OK : cuda_fail(e);
 }
 
+// Up to 64 tokens the weight-row kernel with the narrowest token tile; beyond,
+// the shortest of four estimates.  The times a k-block (us) were fitted to
+// measurements over N, K from 512 to 16384 and 48 to 2048 tokens: weight rows
+// with 128 or 64 tokens to a tile 0.56 and 0.31, a round of SM-pair tiles 0.325
+// (128 wide) and 0.48 (256 wide).  For example 4096 x 11008, 160 tokens:
+// 28.3, 30.8, 31.8 and 44.7 us; 512 tokens: 49.0, 52.5, 32.9, 45.5; 12288 x
+// 4096, 160 tokens: 40.8, 22.4, 26.1, 20.9.
 static pgf8_status block_linear_launch(const BlockLaunch &L)
 {
+    using B16 = BlockCfg<16, 6, 4>;
+    using B32 = BlockCfg<32, 5, 4>;
+    using B64 = BlockCfg<64, 4, 4>;
+    using B128 = BlockCfg<128, 6, 4>;
     if (L.M <= 16)
-        return launch_block<BlockCfg<16, 6, 4>>(L, 2);
+        return launch_block<B16>(L, plan_block<B16>(L, 0.25).splits);
     if (L.M <= 32)
-        return launch_block<BlockCfg<32, 5, 4>>(L, 2);
+        return launch_block<B32>(L, plan_block<B32>(L, 0.27).splits);
+    const BlockPlan p64 = plan_block<B64>(L, 0.31);
     if (L.M <= 64)
-        return launch_block<BlockCfg<64, 4, 4>>(L, 2);
-    if (L.M <= 128)
-        return launch_block<BlockCfg<128, 6, 4>>(L, 1);
-    // 256-wide tiles unless half-width ones fill the rounds of pairs better: a
-    // round of those takes about 0.72 of the time (4096 x 8192 x 10240: 18
-    // rounds in 478 us against 9 in 340; 512 x 4096 x 4096: one in 20.4 us
-    // against one in 24.7)
-    const int64_t pairs = num_sms() / 2, mt = ceil_div(L.M, 256);
-    const int64_t wide = ceil_div(mt * ceil_div(L.N, 256), pairs), narrow = ceil_div(mt * ceil_div(L.N, 128), pairs);
-    if (narrow * 3 < wide * 4)
-        return launch_block_pair<BlockPairCfg<128, 7>>(L);
-    return launch_block_pair<BlockPairCfg<256, 5>>(L);
+        return launch_block<B64>(L, p64.splits);
+    const BlockPlan p128 = plan_block<B128>(L, 0.56);
+    const int64_t pairs = num_sms() / 2, mt = ceil_div(L.M, 256), kb = ceil_div(L.K, 128);
+    const double wide = static_cast<double>(ceil_div(mt * ceil_div(L.N, 256), pairs)) * kb * 0.48;
+    const double narrow = static_cast<double>(ceil_div(mt * ceil_div(L.N, 128), pairs)) * kb * 0.325;
+    if (std::fmin(wide, narrow) < std::fmin(p64.us, p128.us))
+        return narrow < wide ? launch_block_pair<BlockPairCfg<128, 7>>(L) : launch_block_pair<BlockPairCfg<256, 5>>(L);
+    return p64.us < p128.us ? launch_block<B64>(L, p64.splits) : launch_block<B128>(L, p128.splits);
 }
 
 // Shapes, types and pointers of a block-scaled linear layer, activations aside.

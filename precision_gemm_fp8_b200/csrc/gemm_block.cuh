@@ -41,6 +41,7 @@ template <int BN_, int STAGES_, int NBUF_> struct BlockCfg {
     static constexpr int BN = BN_;
     static constexpr int STAGES = STAGES_;
     static constexpr int NBUF = NBUF_;   // accumulator buffers of BN columns
+    static constexpr int CTAS = BN == 128 ? 1 : 2;   // to an SM
     static constexpr int KIND = kE4M3;
     static constexpr int XQ = 0;
     static constexpr int COLS = BN < 32 ? BN : 32;       // tokens of an epilogue thread
@@ -61,7 +62,8 @@ template <int BN_, int STAGES_, int NBUF_> struct BlockCfg {
     static_assert(STAGES <= 8 && NBUF <= 8, "barriers");
     static_assert((kTmemCols & (kTmemCols - 1)) == 0 && kTmemCols <= 512, "tensor memory");
     static_assert(kRingBytes >= BN * 128 * 4, "partial tile");
-    static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+    static_assert(kSmemBytes <= 227 * 1024 && CTAS * (kSmemBytes + 1024) <= 228 * 1024, "shared memory");
+    static_assert(CTAS * kTmemCols <= 512, "tensor memory of an SM");
 };
 
 // Bounded wait for a barrier that another role of the kernel completes within

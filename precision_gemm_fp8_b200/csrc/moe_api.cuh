@@ -75,20 +75,10 @@ static pgf8_status check_moe(const pgf8_fp8_moe_layer &a)
     return PGF8_OK;
 }
 
-// Launches a kernel of cluster size `splits` along z with programmatic stream serialization.
+// Launches a kernel of clusters along z with programmatic stream serialization.
 template <typename... Args>
-static pgf8_status launch_moe(void (*kernel)(Args...), PerDeviceSetup &setup, int max_smem, dim3 grid, int threads,
-                              int smem, cudaStream_t cs, Args... args)
+static pgf8_status launch_moe(void (*kernel)(Args...), dim3 grid, int threads, int smem, cudaStream_t cs, Args... args)
 {
-    const cudaError_t attr_err = setup_once_per_device(setup, [kernel, max_smem](int, int *) {
-        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, max_smem);
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                     cudaSharedmemCarveoutMaxShared);
-        return e;
-    });
-    if (attr_err != cudaSuccess)
-        return cuda_fail(attr_err);
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof(cfg));
     cfg.gridDim = grid;
@@ -101,13 +91,19 @@ static pgf8_status launch_moe(void (*kernel)(Args...), PerDeviceSetup &setup, in
     return e == cudaSuccess ? PGF8_OK : cuda_fail(e);
 }
 
+// kb_us: see stream_plan (two weight tiles a k-block here).
 template <class C>
 static pgf8_status launch_moe_up(const CUtensorMap &tmX, const CUtensorMap &tmW, const MoeUpParams &p, int most,
-                                 cudaStream_t cs)
+                                 double kb_us, cudaStream_t cs)
 {
-    static PerDeviceSetup setup;
-    const int splits = block_splits(static_cast<int64_t>(most) * p.fblocks, p.hblocks, block_slots(C::CTAS));
-    return launch_moe(moe_gate_up_kernel<C>, setup, C::kSmemBytes,
+    static ClusterFit c;
+    const int *fit = nullptr;
+    const cudaError_t e = cluster_fit(c, moe_gate_up_kernel<C>, C::kThreads, C::kSmemBytes, C::kSmemBytes, C::CTAS, fit);
+    if (e != cudaSuccess)
+        return cuda_fail(e);
+    const int64_t tiles = static_cast<int64_t>(most) * p.fblocks;
+    const int splits = stream_plan(tiles, p.hblocks, kb_us, 32768.0 * tiles * p.hblocks, fit).splits;
+    return launch_moe(moe_gate_up_kernel<C>,
                       dim3(static_cast<unsigned>(p.fblocks), static_cast<unsigned>(most),
                            static_cast<unsigned>(splits)),
                       C::kThreads, C::kSmemBytes, cs, tmX, tmW, p);
@@ -115,17 +111,23 @@ static pgf8_status launch_moe_up(const CUtensorMap &tmX, const CUtensorMap &tmW,
 
 template <class C>
 static pgf8_status launch_moe_down(const CUtensorMap &tmH, const CUtensorMap &tmW, const MoeDownParams &p,
-                                   int ctas_per_sm, cudaStream_t cs)
+                                   double kb_us, cudaStream_t cs)
 {
-    static PerDeviceSetup setup;
-    const int hb = (p.H + 127) / 128;
-    const int splits = block_splits(hb, static_cast<int64_t>(p.max_active) * p.fblocks, block_slots(ctas_per_sm));
-    const int plan = p.max_active * 16 + p.pairs * 8;
-    constexpr int kMost = kMoeMaxExperts * 16 + C::BN * kMoeMaxTopK * 8;
-    static_assert(C::kSmemBytes + kMost <= 227 * 1024, "shared memory");
-    return launch_moe(moe_down_kernel<C>, setup, C::kSmemBytes + kMost,
-                      dim3(static_cast<unsigned>(hb), 1, static_cast<unsigned>(splits)), C::kThreads,
-                      C::kSmemBytes + plan, cs, tmH, tmW, p);
+    constexpr int kMost = C::kSmemBytes + kMoeMaxExperts * 16 + C::BN * kMoeMaxTopK * 8;
+    constexpr int kHalf = kMost < 113 * 1024 ? kMost : 113 * 1024;   // two CTAs on an SM
+    static_assert(kMost <= 227 * 1024, "shared memory");
+    const int smem = C::kSmemBytes + p.max_active * 16 + p.pairs * 8;
+    static ClusterFit two, one;
+    const int *fit = nullptr;
+    const bool half = smem <= kHalf;
+    const cudaError_t e = half ? cluster_fit(two, moe_down_kernel<C>, C::kThreads, kMost, kHalf, 2, fit)
+                               : cluster_fit(one, moe_down_kernel<C>, C::kThreads, kMost, kMost, 1, fit);
+    if (e != cudaSuccess)
+        return cuda_fail(e);
+    const int64_t hb = (p.H + 127) / 128, units = static_cast<int64_t>(p.max_active) * p.fblocks;
+    const int splits = stream_plan(hb, units, kb_us, 16384.0 * hb * units, fit).splits;
+    return launch_moe(moe_down_kernel<C>, dim3(static_cast<unsigned>(hb), 1, static_cast<unsigned>(splits)),
+                      C::kThreads, smem, cs, tmH, tmW, p);
 }
 
 } // namespace pgf8
@@ -210,20 +212,20 @@ pgf8_status pgf8_fp8_moe(const pgf8_fp8_moe_layer *layer, int32_t flags, void *s
 
     const MoeUpParams up = {T, F, hblocks, fblocks, f32(ws.sx), a.s13, base + ws.hq, f32(ws.sh), plan};
     if (bn == 16)
-        st = launch_moe_up<MoeUpCfg<16, 3, 4, 2>>(tmX, tmW13, up, most, cs);
+        st = launch_moe_up<MoeUpCfg<16, 3, 4, 2>>(tmX, tmW13, up, most, 0.40, cs);
     else if (bn == 32)
-        st = launch_moe_up<MoeUpCfg<32, 3, 4, 2>>(tmX, tmW13, up, most, cs);
+        st = launch_moe_up<MoeUpCfg<32, 3, 4, 2>>(tmX, tmW13, up, most, 0.45, cs);
     else   // one CTA to an SM: at two, with 96 registers a thread, 64 tokens of 128 experts took 205 us against 166
-        st = launch_moe_up<MoeUpCfg<64, 5, 2, 1>>(tmX, tmW13, up, most, cs);
+        st = launch_moe_up<MoeUpCfg<64, 5, 2, 1>>(tmX, tmW13, up, most, 0.60, cs);
     if (st != PGF8_OK)
         return st;
 
     const MoeDownParams down = {T, H, fblocks, most, pairs, f32(ws.sh), a.s2, a.y, a.ydt, plan};
     if (bn == 16)
-        return launch_moe_down<MoeDownCfg<16, 5, 4>>(tmH, tmW2, down, 2, cs);
+        return launch_moe_down<MoeDownCfg<16, 5, 4>>(tmH, tmW2, down, 0.28, cs);
     if (bn == 32)
-        return launch_moe_down<MoeDownCfg<32, 4, 4>>(tmH, tmW2, down, 2, cs);
-    return launch_moe_down<MoeDownCfg<64, 6, 4>>(tmH, tmW2, down, 1, cs);
+        return launch_moe_down<MoeDownCfg<32, 4, 4>>(tmH, tmW2, down, 0.30, cs);
+    return launch_moe_down<MoeDownCfg<64, 6, 4>>(tmH, tmW2, down, 0.37, cs);
 }
 
 } // extern "C"

@@ -2523,7 +2523,7 @@ const char *pgf8_status_str(pgf8_status s)
     return "unknown status";
 }
 
-int pgf8_version(void) { return 200; }   // 0.2.0: per-tensor scaling, norm / gate fusion, FP8 KV cache and attention
+int pgf8_version(void) { return 300; }   // 0.3.0: block scales, mixture-of-experts layer
 
 } // extern "C"
 
