@@ -167,6 +167,17 @@ __global__ void __launch_bounds__(kQuantThreads)
         scales[row * groups + grp] = g8.d.s;
 }
 
+// g / (1 + e^-g) * u with the reciprocal of the denominator instead of a
+// division: one more rounding and at most one unit in the last place of the
+// hardware reciprocal, about five units of 2^-24 in all, for half the
+// instructions.
+__device__ __forceinline__ float gate_mul(float g, float u)
+{
+    float r;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.0f + expf(-g)));
+    return g * r * u;
+}
+
 // The same for h = silu(gate) * up of gu [rows, 2 inter] (gate = columns
 // [0, inter), up = [inter, 2 inter)); h stays in registers, binary32.
 template <typename T>
@@ -190,7 +201,7 @@ __global__ void __launch_bounds__(kQuantThreads)
         up.load(p + inter);
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-            h[i] = silu_mul(gate.v[i], up.v[i]);
+            h[i] = gate_mul(gate.v[i], up.v[i]);
     }
     const GroupScale g8(h, live);
     if (!live)
