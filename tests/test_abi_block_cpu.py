@@ -85,6 +85,12 @@ def test_moe_arguments():
     assert pg.fp8_moe_workspace_size(65, 256, 128, 8, 2) == 0 and pg.fp8_moe_workspace_size(4, 256, 128, 8, 9) == 0
 
 
+def test_moe_constants_match_the_header():
+    import re
+    values = dict(re.findall(r"\b(PGF8_MOE_[A-Z]+)\s*=\s*(\d+)", open(pg.HEADER_PATH).read()))
+    assert values == {"PGF8_MOE_SOFTMAX": str(pg.MOE_SOFTMAX), "PGF8_MOE_SIGMOID": str(pg.MOE_SIGMOID)}
+
+
 def test_moe_record_matches_the_header():
     """Field order and size of the record as the C struct lays them out."""
     import re
