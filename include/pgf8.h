@@ -737,7 +737,7 @@ size_t pgf8_fp8_block_linear_dynamic_scales_offset(int64_t M, int64_t K);
  *         by their sum when renormalise is set, times factor.  ids [tokens,
  *         top_k] and weights [tokens, top_k] receive the choices, largest
  *         logit first (-1 and 0 where too few can be chosen); either may be
- *         NULL.
+ *         NULL.  A logit of +inf gives the NaN weights that its softmax has.
  *         Without logits (NULL) ids and weights are read.  An id outside
  *         [0, experts) leaves its slot out (padding, another rank's expert); an
  *         expert that a token names twice counts with both weights.
