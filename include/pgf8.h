@@ -695,7 +695,9 @@ pgf8_status pgf8_fp8_silu_mul_quantize_blocks(const void *gu, pgf8_dtype gdt, in
  * pgf8_fp8_block_linear_dynamic: x [M,K] f32, f16 or bf16 (row stride ldx)
  *   is quantised per 1 x 128 group into the workspace (codes at offset 0,
  *   scales at pgf8_fp8_block_linear_dynamic_scales_offset) by a first launch
- *   that the GEMM's weight loads overlap.  workspace:
+ *   that the GEMM's weight loads overlap; for at most 4 tokens without
+ *   PGF8_FLAG_OVERLAP_PREVIOUS the GEMM may do it itself, with the same
+ *   results, and leave the workspace unwritten.  workspace:
  *   pgf8_fp8_block_linear_dynamic_workspace_size(M, K) bytes, 16-byte
  *   aligned, not read before it is written (no zero-fill); one call at a
  *   time may use it.

@@ -77,6 +77,8 @@ struct BlockLaunch {
     int64_t M, N, K;
     int prefetch_w;
     cudaStream_t stream;
+    const void *x = nullptr;   // in-kernel quantisation: the activations, row stride ldx
+    int64_t ldx = 0;
 };
 
 // ------------------------------------------------------------------ kernel choice
@@ -178,6 +180,8 @@ static BlockParams block_params(const BlockLaunch &L)
     p.sw = L.sw;
     p.y = L.y;
     p.ydt = L.ydt;
+    p.x = L.x;
+    p.ldx = L.ldx;
     return p;
 }
 
@@ -214,8 +218,13 @@ template <class C> static pgf8_status launch_block(const BlockLaunch &L, int spl
     if (e != cudaSuccess)
         return cuda_fail(e);
     CUtensorMap tmX, tmW;
-    if (!block_maps<C>(L, tmX, tmW))
+    if constexpr (C::XQ != 0) {
+        std::memset(&tmX, 0, sizeof(tmX));   // not used
+        if (!make_map(&tmW, L.wq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, L.N, L.K, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B))
+            return PGF8_ERR_UNSUPPORTED;
+    } else if (!block_maps<C>(L, tmX, tmW)) {
         return PGF8_ERR_UNSUPPORTED;
+    }
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof(cfg));
     cfg.gridDim = dim3(static_cast<unsigned>(ceil_div(L.N, 128)), static_cast<unsigned>(ceil_div(L.M, C::BN)),
@@ -224,7 +233,7 @@ template <class C> static pgf8_status launch_block(const BlockLaunch &L, int spl
     cfg.dynamicSmemBytes = C::kSmemBytes;
     cfg.stream = L.stream;
     cudaLaunchAttribute attrs[2];
-    fill_attrs(cfg, attrs, splits, 1);
+    fill_attrs(cfg, attrs, splits, C::XQ == 0);   // in-kernel quantisation: an ordinary launch
     e = cudaLaunchKernelEx(&cfg, gemm_block_kernel<C>, tmX, tmW, block_params(L));
     return e == cudaSuccess ? PGF8_OK : cuda_fail(e);
 }
@@ -298,6 +307,30 @@ static pgf8_status block_linear_launch(const BlockLaunch &L)
     if (std::fmin(wide, narrow) < std::fmin(p64.us, p128.us))
         return narrow < wide ? launch_block_pair<BlockPairCfg<128, 7>>(L) : launch_block_pair<BlockPairCfg<256, 5>>(L);
     return p64.us < p128.us ? launch_block<B64>(L, p64.splits) : launch_block<B128>(L, p128.splits);
+}
+
+// At most this many tokens are quantised in the GEMM itself (without
+// PGF8_FLAG_OVERLAP_PREVIOUS: in a chain the quantisation kernel of a layer hides
+// its GEMM's first weight loads behind the layer before).
+constexpr int kBlockFusedTokens = 4;
+
+// The layer from unquantised activations in one launch; the same codes, scales
+// and sums as in two.  False where a CTA's k-blocks would not fit its shared
+// memory, and beyond 32 (token, k-block) groups a CTA, two for each of its
+// epilogue threads' eights: the weights wait for them (12288 x 4096, us on the
+// GPU: one token, 16 groups, 12.6 in one launch and 13.3 in two; two tokens 13.6
+// and 13.8; four tokens, 64 groups, 14.9 and 13.9).
+static bool block_fused_launch(const BlockLaunch &L, int xdt, pgf8_status &st)
+{
+    using B = BlockCfg<16, 6, 4>;
+    const int splits = plan_block<B>(L, 0.25).splits;
+    const int64_t own = ceil_div(ceil_div(L.K, 128), splits);
+    if (L.M > kBlockFusedTokens || own > B::kSlots || L.M * own > 32)
+        return false;
+    st = xdt == PGF8_F32   ? launch_block<BlockCfg<16, 4, 4, 1>>(L, splits)
+         : xdt == PGF8_F16 ? launch_block<BlockCfg<16, 4, 4, 2>>(L, splits)
+                           : launch_block<BlockCfg<16, 4, 4, 3>>(L, splits);
+    return true;
 }
 
 // Shapes, types and pointers of a block-scaled linear layer, activations aside.
@@ -425,11 +458,14 @@ pgf8_status pgf8_fp8_block_linear_dynamic(const void *x, pgf8_dtype xdt, int64_t
     if (st != PGF8_OK)
         return st;
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    // weights may be read early: the quantisation writes only aq / sa, and the
+    // one-launch form follows everything before it
+    BlockLaunch L = {aq, wq, sa, sw, y, ydt, M, N, K, 1, cs, x, ldx};
+    if (!(flags & PGF8_FLAG_OVERLAP_PREVIOUS) && M <= kBlockFusedTokens && block_fused_launch(L, xdt, st))
+        return st;
     st = row_blocks_launch(x, xdt, M, K, ldx, aq, sa, cs, (flags & PGF8_FLAG_OVERLAP_PREVIOUS) ? 1 : 0);
     if (st != PGF8_OK)
         return st;
-    // the quantisation writes only aq / sa: weights may be read while it runs
-    BlockLaunch L = {aq, wq, sa, sw, y, ydt, M, N, K, 1, cs};
     return block_linear_launch(L);
 }
 

@@ -30,6 +30,7 @@
 
 #include "gemm.cuh"
 #include "packed_ptx.cuh"
+#include "quantize_blocks.cuh"
 
 #include <cstddef>
 
@@ -37,25 +38,31 @@ namespace pgf8 {
 
 constexpr int kScaleChunk = 8;   // k-blocks of token scales staged in shared memory at a time
 
-template <int BN_, int STAGES_, int NBUF_> struct BlockCfg {
+// XQ: 0, the activations arrive as codes; 1 / 2 / 3, f32 / f16 / bf16 activations
+// that each CTA quantises itself for its range of K, into shared memory, while
+// its first weight tiles are in flight.  For the few tokens for which that is
+// less work than another launch.
+template <int BN_, int STAGES_, int NBUF_, int XQ_ = 0> struct BlockCfg {
     static constexpr int BN = BN_;
     static constexpr int STAGES = STAGES_;
     static constexpr int NBUF = NBUF_;   // accumulator buffers of BN columns
     static constexpr int CTAS = BN == 128 ? 1 : 2;   // to an SM
     static constexpr int KIND = kE4M3;
-    static constexpr int XQ = 0;
+    static constexpr int XQ = XQ_;
+    static constexpr int kSlots = 20;    // XQ: most k-blocks of a CTA
     static constexpr int COLS = BN < 32 ? BN : 32;       // tokens of an epilogue thread
     static constexpr int kEpi = 128 * (BN / COLS);       // epilogue threads
     static constexpr int kThreads = 64 + kEpi;
     static constexpr int kTileA = 128 * 128;
-    static constexpr int kStage = kTileA + BN * 128;
+    static constexpr int kStage = kTileA + (XQ ? 0 : BN * 128);
     static constexpr int kRowsW = 128;
     static constexpr int kRowsX = BN;
     static constexpr int kTmemCols = NBUF * BN < 32 ? 32 : NBUF * BN;
     static constexpr int kRingBytes = STAGES * kStage;   // reused for the partial tile [BN][128] f32
+    static constexpr int kCodesOffset = kRingBytes;      // XQ: [kSlots][BN][128] codes
     static constexpr int kScalePitch = BN + 4;           // floats; the 8 k-blocks' writes then hit distinct banks
-    static constexpr int kScaleOffset = kRingBytes;
-    static constexpr int kScaleBytes = 2 * kScaleChunk * kScalePitch * 4;
+    static constexpr int kScaleOffset = kCodesOffset + (XQ ? kSlots * BN * 128 : 0);
+    static constexpr int kScaleBytes = (XQ ? kSlots : 2 * kScaleChunk) * kScalePitch * 4;
     static constexpr int kCtlOffset = kScaleOffset + kScaleBytes;
     static constexpr int kSmemBytes = kCtlOffset + 512 + 1024;
     static_assert(BN == 16 || BN == 32 || BN == 64 || BN == 128, "token tile");
@@ -64,6 +71,7 @@ template <int BN_, int STAGES_, int NBUF_> struct BlockCfg {
     static_assert(kRingBytes >= BN * 128 * 4, "partial tile");
     static_assert(kSmemBytes <= 227 * 1024 && CTAS * (kSmemBytes + 1024) <= 228 * 1024, "shared memory");
     static_assert(CTAS * kTmemCols <= 512, "tensor memory of an SM");
+    static_assert(XQ == 0 || BN == 16, "in-kernel quantisation: the narrowest token tile");
 };
 
 // Bounded wait for a barrier that another role of the kernel completes within
@@ -117,6 +125,7 @@ struct BlockCtl {
     uint64_t acc_full[8];
     uint64_t acc_empty[8];
     uint64_t drain;
+    uint64_t codes;          // XQ: this CTA's activation codes are in shared memory
     uint32_t tmem_base;
     int abort;
 };
@@ -128,6 +137,8 @@ struct BlockParams {
     const float *sw;     // [ceil(N / 128), kblocks]
     void *y;             // [M, N]
     int ydt;             // pgf8_dtype
+    const void *x;       // XQ: [M, K], row stride ldx elements
+    int64_t ldx;
 };
 
 // v rounded once to the output type.
@@ -225,6 +236,7 @@ __global__ void __launch_bounds__(C::kThreads)
             mbar_init(&ctl->acc_empty[b], C::kEpi / 32);
         }
         mbar_init(&ctl->drain, 1);
+        mbar_init(&ctl->codes, C::kEpi / 32);
         ctl->abort = 0;
         fence_mbar_init();
     }
@@ -252,8 +264,10 @@ __global__ void __launch_bounds__(C::kThreads)
             }
             if (p.prefetch_w)
                 grid_dependency_wait();
-            for (int i = 0; i < first; ++i)
-                tma_load_2d_hint(smem + i * C::kStage + C::kTileA, &tmX, &ctl->full[i], (kb0 + i) * 128, m0, pol_x);
+            if constexpr (C::XQ == 0)
+                for (int i = 0; i < first; ++i)
+                    tma_load_2d_hint(smem + i * C::kStage + C::kTileA, &tmX, &ctl->full[i], (kb0 + i) * 128, m0,
+                                     pol_x);
             int s = 0;
             uint32_t ph = 0;
             int issued = first;
@@ -263,7 +277,8 @@ __global__ void __launch_bounds__(C::kThreads)
                 uint8_t *st = smem + s * C::kStage;
                 mbar_arrive_expect_tx(&ctl->full[s], C::kStage);
                 tma_load_2d_hint(st, &tmW, &ctl->full[s], kb * 128, n0, pol_w);
-                tma_load_2d_hint(st + C::kTileA, &tmX, &ctl->full[s], kb * 128, m0, pol_x);
+                if constexpr (C::XQ == 0)
+                    tma_load_2d_hint(st + C::kTileA, &tmX, &ctl->full[s], kb * 128, m0, pol_x);
                 ++issued;
                 if (++s == STAGES) {
                     s = 0;
@@ -285,14 +300,17 @@ __global__ void __launch_bounds__(C::kThreads)
             int s = 0, b = 0;
             uint32_t ph = 0, bph = 1;
             bool ok = true;
-            for (int kb = kb0; kb < kb1; ++kb) {
+            if constexpr (C::XQ != 0)
+                ok = __all_sync(0xffffffffu, wait_step(&ctl->codes, 0, abort_flag));
+            for (int kb = kb0; ok && kb < kb1; ++kb) {
                 ok = wait_step(&ctl->acc_empty[b], bph, abort_flag) && wait_step(&ctl->full[s], ph, abort_flag);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok)
                     break;
                 tc_fence_after();
                 const uint32_t a_addr = smem_u32(smem + s * C::kStage);
-                const uint32_t b_addr = a_addr + C::kTileA;
+                const uint32_t b_addr =
+                    C::XQ ? smem_u32(smem + C::kCodesOffset) + (kb - kb0) * (BN * 128) : a_addr + C::kTileA;
                 if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
@@ -348,13 +366,45 @@ __global__ void __launch_bounds__(C::kThreads)
                 pre[i] = (k < kb1 && m < p.M) ? p.sa[static_cast<int64_t>(m) * p.kblocks + k] : 0.0f;
             }
         };
-        fetch(kb0);
+        if constexpr (C::XQ != 0) {
+            // codes and scales of this CTA's k-blocks: 8 threads a group as in the
+            // quantisation kernel, rows of 128 codes in the MMA's swizzled layout
+            // (rows behind the last token hold anything: their columns are not
+            // written out)
+            using T = std::conditional_t<C::XQ == 1, float, std::conditional_t<C::XQ == 2, __half, __nv_bfloat16>>;
+            const int total = (kb1 - kb0) * p.M * 8;
+            for (int base = 0; base < total; base += EPI) {
+                const int i = base + et;
+                const int chunk = i & 7, g = i >> 3;
+                const int kb = g / p.M, m = g - kb * p.M;
+                const int k = (kb0 + kb) * 128 + chunk * 16;
+                const bool live = i < total && k < p.K;
+                Vec16<T> v;
+                if (live)
+                    v.load(static_cast<const T *>(p.x) + static_cast<int64_t>(m) * p.ldx + k);
+                const GroupScale g8(v.v, live);
+                if (i < total) {
+                    *reinterpret_cast<uint4 *>(smem + C::kCodesOffset + kb * (BN * 128) + m * 128 +
+                                               ((chunk ^ (m & 7)) << 4)) =
+                        live ? g8.encode(v.v) : make_uint4(0u, 0u, 0u, 0u);
+                    if (chunk == 0)
+                        sc[kb * C::kScalePitch + m] = g8.d.s * __ldg(swr + kb0 + kb);
+                }
+            }
+            fence_proxy_async_smem();   // each writer, before the MMA (async proxy) reads
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&ctl->codes);
+            bar_sync_epilogue<EPI>();   // the scales
+        } else {
+            fetch(kb0);
+        }
         int b = 0;
         uint32_t bph = 0;
         bool ok = true;
         for (int i = 0; i < kb1 - kb0; ++i) {
             float *buf = sc + ((i / kScaleChunk) & 1) * kScaleChunk * C::kScalePitch;
-            if (i % kScaleChunk == 0) {
+            if (C::XQ == 0 && i % kScaleChunk == 0) {
 #pragma unroll
                 for (int j = 0; j < PER; ++j)
                     buf[(et & 7) * C::kScalePitch + ((et + EPI * j) >> 3)] = pre[j] * wgt;
@@ -366,7 +416,9 @@ __global__ void __launch_bounds__(C::kThreads)
             ok = __all_sync(0xffffffffu, ok);
             if (ok) {
                 tc_fence_after();
-                add_scaled<COLS>(t_row + b * BN, buf + (i % kScaleChunk) * C::kScalePitch + col0, acc);
+                add_scaled<COLS>(t_row + b * BN,
+                                 (C::XQ ? sc + i * C::kScalePitch : buf + (i % kScaleChunk) * C::kScalePitch) + col0,
+                                 acc);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
