@@ -316,9 +316,8 @@ constexpr int kBlockFusedTokens = 4;
 
 // The layer from unquantised activations in one launch; the same codes, scales
 // and sums as in two.  False where a CTA's k-blocks would not fit its shared
-// memory, and beyond 32 (token, k-block) groups a CTA, two for each of its
-// epilogue threads' eights: the weights wait for them (12288 x 4096, us on the
-// GPU: one token, 16 groups, 12.6 in one launch and 13.3 in two; two tokens 13.6
+// memory, and beyond 32 (token, k-block) groups a CTA, two for each eight of its
+// epilogue threads: the weights wait for them (12288 x 4096, us on the GPU: one token, 16 groups, 12.6 in one launch and 13.3 in two; two tokens 13.6
 // and 13.8; four tokens, 64 groups, 14.9 and 13.9).
 static bool block_fused_launch(const BlockLaunch &L, int xdt, pgf8_status &st)
 {
