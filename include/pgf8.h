@@ -736,7 +736,8 @@ size_t pgf8_fp8_block_linear_dynamic_scales_offset(int64_t M, int64_t K);
  *         logits, ties to the lower index; NaN and -inf are never chosen.  The
  *         weights are the chosen experts' shares of the softmax over all
  *         experts (PGF8_MOE_SOFTMAX) or their sigmoids (PGF8_MOE_SIGMOID), divided
- *         by their sum when renormalise is set, times factor.  ids [tokens,
+ *         by their sum when renormalise is set (sigmoids far below zero, whose
+ *         sum vanishes in binary32, keep their shares), times factor.  ids [tokens,
  *         top_k] and weights [tokens, top_k] receive the choices, largest
  *         logit first (-1 and 0 where too few can be chosen); either may be
  *         NULL.  A logit of +inf gives the NaN weights that its softmax has.

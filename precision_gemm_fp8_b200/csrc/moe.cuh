@@ -70,6 +70,29 @@ __device__ __forceinline__ uint32_t logit_key(float v)
     return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
+__device__ __forceinline__ float key_logit(uint32_t key)
+{
+    return __uint_as_float((key & 0x80000000u) ? key & 0x7FFFFFFFu : ~key);
+}
+
+// Sigmoids of a token that has chosen a logit below kFarLogit (lane j: choice j,
+// the largest first).  There 1 + e^-f overflows sooner than e^f / (1 + e^f)
+// vanishes, and the shares of such sigmoids are ordinary numbers although the
+// sigmoids may all be below the smallest one: with renorm they are taken
+// relative to the largest, which goes out with the division by their sum.
+// Not inlined: rare, and inlined it takes the plan kernel from 64 to 76
+// registers a thread.
+constexpr float kFarLogit = -64.0f;
+
+__device__ __noinline__ float far_sigmoid(bool chosen, float f, int renorm)
+{
+    const float largest = __shfl_sync(0xffffffffu, f, 0);
+    const float unit = renorm && largest < 0.0f ? largest : 0.0f;
+    if (!chosen)
+        return 0.0f;
+    return f > 0.0f ? __fdiv_rn(1.0f, 1.0f + expf(-f)) : __fdiv_rn(expf(f - unit), 1.0f + expf(f));
+}
+
 __device__ __forceinline__ void st_shared_cluster_u32(uint32_t addr, uint32_t v)
 {
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
@@ -145,9 +168,11 @@ __device__ __forceinline__ void route_token(const MoeRouteParams &p, int t, uint
     }
     float mine = 0.0f;
     if (my_id >= 0) {
-        const float f = __uint_as_float((my_key & 0x80000000u) ? my_key & 0x7FFFFFFFu : ~my_key);
+        const float f = key_logit(my_key);
         mine = p.score == kMoeSoftmax ? __fdiv_rn(expf(f - top), sum) : __fdiv_rn(1.0f, 1.0f + expf(-f));
     }
+    if (p.score != kMoeSoftmax && __any_sync(0xffffffffu, my_id >= 0 && key_logit(my_key) < kFarLogit))
+        mine = far_sigmoid(my_id >= 0, key_logit(my_key), p.renorm);
     if (p.renorm) {
         float all = mine;
 #pragma unroll

@@ -57,3 +57,50 @@ def test_gate_of_infinities_nans_and_zeros(dt):
         nan = (rq[i] & 0x7F) == 0x7F
         assert np.array_equal((q[i] & 0x7F) == 0x7F, nan), pair
         assert np.array_equal(q[i][~nan], rq[i][~nan]), pair
+
+
+def _sigmoid_shares(logits, k, renorm):
+    """(ids, weights) in binary64 by logarithms: nothing overflows or vanishes."""
+    v = logits.astype(np.float64)
+    ids = np.argsort(-v, axis=1, kind="stable")[:, :k].astype(np.int32)
+    w = -np.logaddexp(0.0, -np.take_along_axis(v, ids, 1))     # log sigmoid
+    if renorm:
+        top = w.max(1, keepdims=True)
+        w = (w - top) - np.log(np.exp(w - top).sum(1, keepdims=True))   # a top of -3e38 would swallow the logarithm
+    return ids, np.exp(w)
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+def test_moe_sigmoid_routing_of_far_logits(renorm):
+    """Sigmoids far below binary32's smallest value still have shares: logits
+    from -60 to the type's lowest, alone and beside ordinary ones.  Weights
+    within the roundings of two exponentials of arguments up to 400 (half a step
+    of the argument each: at most 2^-16 of the result), a sum of k terms, two
+    quotients and two products, or two steps of the smallest subnormal."""
+    T, E, k, H, F = 9, 8, 3, 128, 16
+    g = np.random.default_rng(3)
+    v = np.full((T, E), -500.0, np.float32)
+    v[0, :2] = -95.0, -96.0
+    v[1] = -200 - np.arange(E) * 0.75
+    v[2, :3] = -87.0, -88.5, -89.25
+    v[3] = np.finfo(np.float32).min
+    v[4, :3] = 1.5, -70.0, -100.0
+    v[5, :3] = -20.0, -95.0, -100.0
+    v[6, :3] = -29.0, -31.0, -66.0
+    v[7, :3] = -64.0, -64.5, -63.5
+    v[8, :3] = -1e30, -1e30, -100.0
+    q13 = np.zeros((E, 2 * F, H), np.uint8)
+    q13[:, :F] = q13[:, F:] = oracle.e4m3_encode_array(np.array([0.25], np.float32))[0]
+    w = (q13, np.ones((E, 2, 1, 1), np.float32), np.full((E, H, F), q13[0, 0, 0], np.uint8),
+         np.ones((E, 1, 1), np.float32))
+    x = g.integers(1, 3, (T, H)).astype(np.float32)
+    x[:, 0] = 448
+    y, ids, wt = pg.fp8_moe(_to(x), *(_to(t) for t in w), logits=_to(v), top_k=k, score=pg.MOE_SIGMOID,
+                            renormalise=renorm, out_dtype=torch.float32)
+    _done()
+    rid, rw = _sigmoid_shares(v, k, renorm)
+    assert np.array_equal(_np(ids), rid)
+    got = _np(wt).astype(np.float64)
+    assert np.all(np.abs(got - rw) <= (2.0 ** -15 + (k + 16) * 2.0 ** -24) * rw + 2.0 ** -148), (got, rw)
+    if renorm:
+        assert np.all(np.abs(got.sum(1) - 1) <= (k + 1) * 2.0 ** -24) and bool((y != 0).all())
