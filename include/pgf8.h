@@ -685,8 +685,12 @@ pgf8_status pgf8_fp8_silu_mul_quantize_blocks(const void *gu, pgf8_dtype gdt, in
  * wq [N,K] codes with sw [ceil(N/128), ceil(K/128)] (one per 128 x 128
  * block), as pgf8_fp8_quantize_blocks writes them; y [M,N] contiguous, ydt f32,
  * f16 or bf16.  The products of a block and the sum over blocks are
- * accumulated in binary32 and rounded once to ydt.  Scales may be any finite
- * values.  0 <= M <= 2^23 (M == 0: no-op); K % 16 == 0, N % 16 == 0, any
+ * accumulated in binary32 and rounded once to ydt.  A block's sum is
+ * multiplied by the product sa[m,b] * sw[n / 128, b], rounded to binary32:
+ * that product has to be 0 or between 2^-126 and 2^128 in magnitude (it always
+ * is where the largest value of every block lies between 2^-50 and 2^60).
+ * Beyond, it overflows as binary32 does (NaN with a sum of 0), or loses bits.
+ * 0 <= M <= 2^23 (M == 0: no-op); K % 16 == 0, N % 16 == 0, any
  * relation of K and N to 128.  aq, wq and y 16-byte aligned.  No workspace;
  * calls on different streams may run at once.  Deterministic.
  *
@@ -720,7 +724,8 @@ size_t pgf8_fp8_block_linear_dynamic_scales_offset(int64_t M, int64_t K);
  *     y[t] += w[t,e] * (hq . W2[e]^T)
  * with xq and hq the E4M3 codes of x and h, one scale per 1 x 128 group (as
  * pgf8_fp8_quantize_blocks), every product scaled block by block as in
- * pgf8_fp8_block_linear, the sum over experts in binary32 in ascending order
+ * pgf8_fp8_block_linear (the down product by (scale of hq * s2) * w, and the
+ * same range holds for both steps of it), the sum over experts in binary32 in ascending order
  * of e and one rounding to ydt.
  *
  * x       [tokens, hidden] f32, f16 or bf16, row stride ldx; tokens 0..64

@@ -952,7 +952,9 @@ def fp8_block_linear(aq: torch.Tensor, sa: torch.Tensor, wq: torch.Tensor, sw: t
                      stream=None) -> torch.Tensor:
     """y [M, N] (f32, f16 or bf16: y's type, or out_dtype) of E4M3 activations
     aq [M, K] with scales sa [M, ceil(K / 128)] and E4M3 weights wq [N, K] with
-    scales sw [ceil(N / 128), ceil(K / 128)], as fp8_quantize_blocks gives them."""
+    scales sw [ceil(N / 128), ceil(K / 128)], as fp8_quantize_blocks gives them.
+    A product sa * sw of scales that meet has to be 0 or between 2^-126 and 2^128
+    in magnitude."""
     if aq.dim() != 2:
         raise ValueError("aq must be [M, K]")
     M, K = aq.shape

@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import oracle
+from _blocks import linear, linear_bound, moe, up
 
 pg = pytest.importorskip("precision_gemm_fp8_b200")
 pytestmark = pytest.mark.gpu
@@ -104,3 +105,91 @@ def test_moe_sigmoid_routing_of_far_logits(renorm):
     assert np.all(np.abs(got - rw) <= (2.0 ** -15 + (k + 16) * 2.0 ** -24) * rw + 2.0 ** -148), (got, rw)
     if renorm:
         assert np.all(np.abs(got.sum(1) - 1) <= (k + 1) * 2.0 ** -24) and bool((y != 0).all())
+
+
+def _far_scales(m, n, k, seed):
+    """Tokens and weight blocks of three kinds: ordinary, large (scales 2^70 and
+    2^56 times 1 to 2, small codes, some tokens' all zero) and small (2^-70 and
+    2^-56, codes up to 448).  Where two of a kind meet, the scales' products reach the
+    ends of binary32's normal range, and results are normal numbers or exact zeros."""
+    g = np.random.default_rng(seed)
+    codes = lambda top, shape: oracle.e4m3_encode_array(  # noqa: E731
+        (g.choice([-1.0, 1.0, 1.0, 1.0], shape) * top * g.choice([0.5, 0.75, 1.0], shape)).astype(np.float32))
+    aq, wq = codes(1.0, (m, k)), codes(1.0, (n, k))
+    # up to 1.41: 2^127 times two of them stays below 2^128
+    sa, sw = (1 + 0.41 * g.random((m, up(k)))).astype(np.float32), (1 + 0.41 * g.random((up(n), up(k)))).astype(np.float32)
+    for i in range(m):
+        if i % 4 == 0:
+            aq[i], sa[i] = codes(448.0, k), np.ldexp(sa[i], -70)
+        elif i % 4 in (1, 2):
+            aq[i], sa[i] = codes(2.0 ** -7, k) * (i % 4 == 1), np.ldexp(sa[i], 70)
+    for j in range(up(n)):
+        at = np.s_[j * 128:(j + 1) * 128]
+        if j % 3 == 1:
+            wq[at], sw[j] = codes(448.0, wq[at].shape), np.ldexp(sw[j], -56)
+        elif j % 3 == 2:
+            wq[at], sw[j] = codes(2.0 ** -7, wq[at].shape), np.ldexp(sw[j], 57)
+    return aq, sa, wq, sw
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 400, 1040), (3, 272, 400), (7, 528, 2064), (20, 400, 784), (60, 656, 1040),
+                                   (90, 4096, 656), (100, 400, 1168), (300, 528, 1040), (520, 1296, 400),
+                                   (700, 4096, 656)])
+def test_block_linear_scales_at_the_ends_of_the_range(m, n, k):
+    """A step of the smallest subnormal for each addition beside the linear bound."""
+    c = _far_scales(m, n, k, m + n)
+    factors = c[1].astype(np.float64)[:, None] * c[3].astype(np.float64)
+    assert (m == 1 or 2.0 ** 127 <= factors.max()) and factors.max() < 2.0 ** 128 and 2.0 ** -126 <= factors.min() < 2.0 ** -124
+    y = pg.fp8_block_linear(*(_to(t) for t in c), out_dtype=torch.float32)
+    _done()
+    ref, mag = linear(*c)
+    assert mag.max() < 2.0 ** 127
+    err = np.abs(_np(y).astype(np.float64) - ref)
+    bound = linear_bound(ref, mag, k, "f32") + (up(k) + 10) * 2.0 ** -149
+    assert np.all(err <= bound), (err / bound).max()
+
+
+def test_block_linear_zero_and_infinite_scales_keep_their_meaning():
+    """A zero scale gives zeros beside any finite one, an infinite scale no
+    finite value, whatever the size of the other."""
+    m, n, k = 6, 256, 384
+    g = np.random.default_rng(0)
+    aq = oracle.e4m3_encode_array(g.integers(1, 3, (m, k)).astype(np.float32))
+    wq = oracle.e4m3_encode_array(g.integers(1, 3, (n, k)).astype(np.float32))
+    sa, sw = np.zeros((m, 3), np.float32), np.full((2, 3), 2.0 ** 100, np.float32)
+    sa[1] = 2.0 ** -60
+    sa[2, 1] = np.inf
+    sa[3, 2] = np.nan
+    y = _np(pg.fp8_block_linear(_to(aq), _to(sa), _to(wq), _to(sw), out_dtype=torch.float32))
+    _done()
+    assert not y[[0, 4, 5]].any() and np.isfinite(y[1]).all() and not np.isfinite(y[2]).any() and np.isnan(y[3]).all()
+
+
+@pytest.mark.parametrize("T", [1, 20, 40])
+def test_moe_down_scales_at_the_ends_of_the_range(T):
+    """The product of the hidden scale, W2's and the routing weight, with hidden
+    codes that do not depend on the order of sums (gates of 28 and more, where
+    silu(g) = g), near either end of binary32's range."""
+    E, k, H, F = 3, 3, 144, 272
+    g = np.random.default_rng(T)
+    val = lambda v: int(oracle.e4m3_encode_array(np.array([v], np.float32))[0])  # noqa: E731
+    small = oracle.e4m3_encode_array(np.arange(1, 4).astype(np.float32))
+    x = g.integers(-2, 3, (T, H)).astype(np.float32)
+    x[:, ::128] = 448
+    w13 = np.zeros((E, 2 * F, H), np.uint8)
+    w13[:, :F, ::128] = val(1 / 16)
+    w13[:, F:] = small[g.integers(0, 3, (E, F, H))]
+    w2 = small[g.integers(0, 3, (E, H, F))]
+    s2 = (1 + g.random((E, up(H), up(F)))).astype(np.float32)
+    s2[0], s2[1], s2[2] = np.ldexp(s2[0], -100), np.ldexp(s2[1], 100), np.ldexp(s2[2], -60)
+    wt = np.ldexp(1 + g.random((T, k)), [[-20, -120, 8]]).astype(np.float32)
+    ids = np.tile(np.arange(3, dtype=np.int32), (T, 1))
+    w = (w13, np.ones((E, 2, up(F), up(H)), np.float32), w2, s2)
+    for keep in range(3):
+        one = np.where(np.arange(3) == keep, ids, -1).astype(np.int32)
+        y, _, _ = pg.fp8_moe(_to(x), *(_to(t) for t in w), ids=_to(one), weights=_to(wt), out_dtype=torch.float32)
+        _done()
+        ref, off = moe(x, *w, one, wt, exact_hidden=True)
+        y = _np(y).astype(np.float64)
+        bound = off + 2.0 ** -24 * np.abs(ref) + 2.0 ** -149 * (up(F) + 10)
+        assert np.all(np.abs(y - ref) <= bound), (keep, (np.abs(y - ref) / bound).max())
