@@ -701,7 +701,9 @@ pgf8_status pgf8_fp8_silu_mul_quantize_blocks(const void *gu, pgf8_dtype gdt, in
  *   scales at pgf8_fp8_block_linear_dynamic_scales_offset) by a first launch
  *   that the GEMM's weight loads overlap; for at most 4 tokens without
  *   PGF8_FLAG_OVERLAP_PREVIOUS the GEMM may do it itself, with the same
- *   results, and leave the workspace unwritten.  workspace:
+ *   results, and leave the workspace unwritten.  y may lie over x (a layer in
+ *   place); else outputs are apart from the inputs, here and in all calls of
+ *   this section.  workspace:
  *   pgf8_fp8_block_linear_dynamic_workspace_size(M, K) bytes, 16-byte
  *   aligned, not read before it is written (no zero-fill); one call at a
  *   time may use it.

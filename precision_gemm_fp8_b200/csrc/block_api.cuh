@@ -316,15 +316,21 @@ constexpr int kBlockFusedTokens = 4;
 
 // The layer from unquantised activations in one launch; the same codes, scales
 // and sums as in two.  False where a CTA's k-blocks would not fit its shared
-// memory, and beyond 32 (token, k-block) groups a CTA, two for each eight of its
-// epilogue threads: the weights wait for them (12288 x 4096, us on the GPU: one token, 16 groups, 12.6 in one launch and 13.3 in two; two tokens 13.6
-// and 13.8; four tokens, 64 groups, 14.9 and 13.9).
+// memory, where y lies over x, and beyond 32 (token, k-block) groups a CTA, two
+// for each eight of its epilogue threads: the weights wait for them (12288 x
+// 4096, us on the GPU: one token, 16 groups, 12.6 in one launch and 13.3 in two;
+// two tokens 13.6 and 13.8; four tokens, 64 groups, 14.9 and 13.9).
 static bool block_fused_launch(const BlockLaunch &L, int xdt, pgf8_status &st)
 {
     using B = BlockCfg<16, 6, 4>;
     const int splits = plan_block<B>(L, 0.25).splits;
     const int64_t own = ceil_div(ceil_div(L.K, 128), splits);
     if (L.M > kBlockFusedTokens || own > B::kSlots || L.M * own > 32)
+        return false;
+    // every CTA reads x, some of them after others have written their part of y
+    const uintptr_t x = reinterpret_cast<uintptr_t>(L.x), y = reinterpret_cast<uintptr_t>(L.y);
+    if (x < y + static_cast<uintptr_t>(L.M * L.N * dtype_bytes(L.ydt)) &&
+        y < x + static_cast<uintptr_t>(((L.M - 1) * L.ldx + L.K) * dtype_bytes(xdt)))
         return false;
     st = xdt == PGF8_F32   ? launch_block<BlockCfg<16, 4, 4, 1>>(L, splits)
          : xdt == PGF8_F16 ? launch_block<BlockCfg<16, 4, 4, 2>>(L, splits)

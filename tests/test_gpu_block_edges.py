@@ -193,3 +193,19 @@ def test_moe_down_scales_at_the_ends_of_the_range(T):
         y = _np(y).astype(np.float64)
         bound = off + 2.0 ** -24 * np.abs(ref) + 2.0 ** -149 * (up(F) + 10)
         assert np.all(np.abs(y - ref) <= bound), (keep, (np.abs(y - ref) / bound).max())
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("m", [1, 2, 4, 5, 40, 300])
+def test_block_linear_dynamic_in_place(m, dt):
+    """y may be x, or lie over part of it: x is quantised before a row of y is written."""
+    k = n = 1040
+    g = torch.Generator(device=DEV).manual_seed(m)
+    wq, sw = pg.fp8_quantize_blocks(torch.randn((n, k), generator=g, device=DEV) * 0.02, block_rows=128)
+    x = torch.randn((m + 1, k), generator=g, device=DEV).to(DT[dt])
+    for at in (0, 1):                      # the same rows; the second overlaps by all but one
+        z = x.clone()
+        want = pg.fp8_block_linear_dynamic(z[:m], wq, sw, out_dtype=DT[dt])
+        y = pg.fp8_block_linear_dynamic(z[:m], wq, sw, y=z[at:at + m])
+        _done()
+        assert torch.equal(y, want) and (at == 0 or torch.equal(z[0], x[0]))
