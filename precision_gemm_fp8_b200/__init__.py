@@ -784,6 +784,12 @@ class NestedLayerGroup:
 
 
 # ----------------------------------------------------------------- block scales
+def _row_stride(t: torch.Tensor) -> int:
+    """Elements from row to row of a 2-D tensor; its width where there is one row
+    at most, whose stride may be any number."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
 _DTYPES = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
 
 
@@ -867,8 +873,10 @@ def fp8_quantize_blocks(x: torch.Tensor, block_rows: int = 1, q: torch.Tensor | 
     # a dimension of one entry may carry any stride
     if dims == 3:
         batch = shape[0]
-        ldx = strides[1] if rows > 1 else max(cols, strides[0] if block_rows == 1 else 0)
+        ldx = strides[1] if rows > 1 else cols
         ldb = strides[0] if batch > 1 else rows * ldx
+        if block_rows == 1 and rows == 1 and batch > 1 and ldb >= cols:
+            ldx = ldb                 # one row each: the matrices' stride is the rows'
         sshape = (batch, -(-rows // block_rows), -(-cols // 128))
     else:
         batch, ldb = 1, 0
@@ -914,7 +922,7 @@ def fp8_silu_mul_quantize_blocks(gu: torch.Tensor, q: torch.Tensor | None = None
             scales = gu.new_empty((rows, _blocks(inter)), dtype=torch.float32)
         else:
             _want(scales, (rows, _blocks(inter)), torch.float32, "scales")
-        _check(lib.pgf8_fp8_silu_mul_quantize_blocks(gu.data_ptr(), code, rows, inter, _lead(gu), q.data_ptr(),
+        _check(lib.pgf8_fp8_silu_mul_quantize_blocks(gu.data_ptr(), code, rows, inter, _row_stride(gu), q.data_ptr(),
                                                      scales.data_ptr(), flags, handle),
                "fp8_silu_mul_quantize_blocks")
     finally:
@@ -989,7 +997,7 @@ def fp8_block_linear_dynamic(x: torch.Tensor, wq: torch.Tensor, sw: torch.Tensor
     try:
         y, code = _block_out(y, (M, N), out_dtype, x)
         workspace, nbytes = _workspace(workspace, lib.pgf8_fp8_block_linear_dynamic_workspace_size(M, K), x)
-        _check(lib.pgf8_fp8_block_linear_dynamic(x.data_ptr(), xcode, M, K, _lead(x) if M else K, wq.data_ptr(),
+        _check(lib.pgf8_fp8_block_linear_dynamic(x.data_ptr(), xcode, M, K, _row_stride(x), wq.data_ptr(),
                                                  sw.data_ptr(), N, y.data_ptr(), code, workspace.data_ptr(),
                                                  nbytes, flags, handle), "fp8_block_linear_dynamic")
     finally:
@@ -1034,7 +1042,7 @@ def fp8_moe(x: torch.Tensor, w13: torch.Tensor, s13: torch.Tensor, w2: torch.Ten
             raise ValueError("routing from logits needs top_k")
         if logits.shape != (T, E) or (E > 1 and logits.stride(1) != 1):
             raise ValueError(f"logits must be [{T}, {E}] with contiguous rows")
-        lcode, ldl = _code(logits.dtype, "logits"), _lead(logits) if T else E
+        lcode, ldl = _code(logits.dtype, "logits"), _row_stride(logits)
     else:
         if ids is None or weights is None:
             raise ValueError("fp8_moe needs logits and top_k, or ids and weights")
@@ -1057,7 +1065,7 @@ def fp8_moe(x: torch.Tensor, w13: torch.Tensor, s13: torch.Tensor, w2: torch.Ten
         layer = MoeLayer(x.data_ptr(), w13.data_ptr(), s13.data_ptr(), w2.data_ptr(), s2.data_ptr(),
                          None if logits is None else logits.data_ptr(), ids.data_ptr(), weights.data_ptr(),
                          y.data_ptr(), workspace.data_ptr(), nbytes, T, H, F, E, top_k,
-                         _lead(x) if T else H, ldl, xcode, lcode, ycode, score, 1 if renormalise else 0, factor)
+                         _row_stride(x), ldl, xcode, lcode, ycode, score, 1 if renormalise else 0, factor)
         _check(lib.pgf8_fp8_moe(ctypes.byref(layer), flags, handle), "fp8_moe")
     finally:
         _leave(back)

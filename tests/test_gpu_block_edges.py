@@ -209,3 +209,32 @@ def test_block_linear_dynamic_in_place(m, dt):
         y = pg.fp8_block_linear_dynamic(z[:m], wq, sw, y=z[at:at + m])
         _done()
         assert torch.equal(y, want) and (at == 0 or torch.equal(z[0], x[0]))
+
+
+def _odd_row(width, dt):
+    """One row of `width` values whose stride is no multiple of 16 bytes (and of no meaning: there is one row)."""
+    big = torch.randn((3, width + 1), generator=torch.Generator().manual_seed(width)).to(DT[dt]).to(DEV)
+    view = torch.empty(width + 64, dtype=DT[dt], device=DEV)[:width].view(1, width)
+    view.copy_(big[1:2, :width])
+    return view.as_strided((1, width), (width + 3, 1))
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_one_row_may_carry_any_stride(dt):
+    x = _odd_row(512, dt)
+    plain = x.clone(memory_format=torch.contiguous_format).as_strided((1, 512), (512, 1))
+    same = lambda a, b: all(torch.equal(s, t) for s, t in zip(a, b))  # noqa: E731
+    assert x.stride(0) == 515
+    for rows in (1, 128):
+        assert same(pg.fp8_quantize_blocks(x, block_rows=rows), pg.fp8_quantize_blocks(plain, block_rows=rows))
+        x3 = x.as_strided((1, 1, 512), (1031, 515, 1))
+        assert same(pg.fp8_quantize_blocks(x3, block_rows=rows), pg.fp8_quantize_blocks(plain[None], block_rows=rows))
+    assert same(pg.fp8_silu_mul_quantize_blocks(x), pg.fp8_silu_mul_quantize_blocks(plain))
+    wq, sw = pg.fp8_quantize_blocks(torch.randn((144, 512), device=DEV), block_rows=128)
+    assert torch.equal(pg.fp8_block_linear_dynamic(x, wq, sw), pg.fp8_block_linear_dynamic(plain, wq, sw))
+    w13, s13 = pg.fp8_quantize_blocks(torch.randn((4, 128, 512), device=DEV), block_rows=128)
+    w2, s2 = pg.fp8_quantize_blocks(torch.randn((2, 512, 128), device=DEV), block_rows=128)
+    w = (w13.view(2, 256, 512), s13.view(2, 2, 1, 4), w2, s2)
+    lg = torch.randn((1, 2), device=DEV)
+    assert same(pg.fp8_moe(x, *w, logits=lg, top_k=1), pg.fp8_moe(plain, *w, logits=lg, top_k=1))
+    _done()
