@@ -860,8 +860,10 @@ def fp8_quantize_blocks(x: torch.Tensor, block_rows: int = 1, q: torch.Tensor | 
     """E4M3 quantisation of x [rows, cols] or [batch, rows, cols] (f32, f16,
     bf16; rows and matrices may be strided) with one scale per 1 x 128 group of
     a row (block_rows 1: activations) or per 128 x 128 block (block_rows 128:
-    weights).  Returns (q uint8 of x's shape, scales f32 [.., ceil(rows /
-    block_rows), ceil(cols / 128)])."""
+    weights).  One launch; with block_rows 1, a launch for each matrix of a batch
+    whose matrices do not follow one another (x[::2], x[:, :rows]).  Returns (q
+    uint8 of x's shape, scales f32 [.., ceil(rows / block_rows), ceil(cols /
+    128)])."""
     shape = x.shape
     dims = len(shape)
     if dims not in (2, 3) or block_rows not in (1, 128):
@@ -882,6 +884,10 @@ def fp8_quantize_blocks(x: torch.Tensor, block_rows: int = 1, q: torch.Tensor | 
         batch, ldb = 1, 0
         ldx = strides[0] if rows > 1 else cols
         sshape = (-(-rows // block_rows), -(-cols // 128))
+    # row groups of matrices that do not follow one another: a launch for each
+    apart = block_rows == 1 and batch > 1 and rows > 0 and ldb != rows * ldx
+    if apart and ldb * x.element_size() % 16:
+        raise Pgf8Error(ERR_ALIGNMENT, "fp8_quantize_blocks")
     code = _code(x.dtype, "x")
     device = x.device
     _same_device(device, q, scales)
@@ -895,8 +901,11 @@ def fp8_quantize_blocks(x: torch.Tensor, block_rows: int = 1, q: torch.Tensor | 
             scales = x.new_empty(sshape, dtype=torch.float32)
         else:
             _want(scales, sshape, torch.float32, "scales")
-        _check(lib.pgf8_fp8_quantize_blocks(x.data_ptr(), code, batch, rows, cols, ldx, ldb, block_rows,
-                                            q.data_ptr(), scales.data_ptr(), flags, handle), "fp8_quantize_blocks")
+        xp, qp, sp = x.data_ptr(), q.data_ptr(), scales.data_ptr()
+        for _ in range(batch if apart else 1):
+            _check(lib.pgf8_fp8_quantize_blocks(xp, code, 1 if apart else batch, rows, cols, ldx, ldb, block_rows,
+                                                qp, sp, flags, handle), "fp8_quantize_blocks")
+            xp, qp, sp = xp + ldb * x.element_size(), qp + rows * cols, sp + 4 * rows * sshape[-1]
     finally:
         _leave(back)
     return q, scales

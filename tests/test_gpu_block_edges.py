@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import oracle
-from _blocks import linear, linear_bound, moe, up
+from _blocks import encode, linear, linear_bound, moe, up
 
 pg = pytest.importorskip("precision_gemm_fp8_b200")
 pytestmark = pytest.mark.gpu
@@ -238,3 +238,34 @@ def test_one_row_may_carry_any_stride(dt):
     lg = torch.randn((1, 2), device=DEV)
     assert same(pg.fp8_moe(x, *w, logits=lg, top_k=1), pg.fp8_moe(plain, *w, logits=lg, top_k=1))
     _done()
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16"])
+def test_quantize_row_groups_of_strided_batches(dt):
+    """1 x 128 groups of matrices that do not follow one another: every second
+    one, their first rows, the same one again, one row each; in given buffers."""
+    stack = torch.randn((6, 150, 144), generator=torch.Generator().manual_seed(1)).to(DT[dt]).to(DEV)
+    for x in (stack[::2], stack[:, :140], stack[1:5, 3:4], stack[::3, 5:6, :128], stack[2:3].expand(3, 150, 144),
+              stack[:, :, 16:], stack[:0, :140]):
+        q, s = pg.fp8_quantize_blocks(x)
+        rq, rs = pg.fp8_quantize_blocks(x.contiguous())
+        q2 = torch.full((x.shape[0] + 2, *x.shape[1:]), 0xEE, dtype=torch.uint8, device=DEV)
+        s2 = torch.full((x.shape[0] + 2, x.shape[1], up(x.shape[2])), -1.0, device=DEV)
+        pg.fp8_quantize_blocks(x, q=q2[1:-1], scales=s2[1:-1], flags=pg.FLAG_OVERLAP_PREVIOUS)
+        _done()
+        assert torch.equal(q, rq) and torch.equal(s, rs) and torch.equal(q2[1:-1], rq) and torch.equal(s2[1:-1], rs)
+        for edge in (q2[0], q2[-1]):
+            assert bool((edge == 0xEE).all())
+        assert bool((s2[0] == -1).all()) and bool((s2[-1] == -1).all())
+        for i in range(x.shape[0]):
+            eq, es = encode(_np(x[i].float()), 1)
+            assert np.array_equal(_np(q[i]), eq) and np.array_equal(_np(s[i]), es)
+
+
+def test_quantize_row_groups_refuses_a_misaligned_batch_before_any_launch():
+    x = torch.zeros(600, device=DEV).as_strided((2, 2, 128), (258, 128, 1))     # the second matrix at 1032 bytes
+    q = torch.full((2, 2, 128), 7, dtype=torch.uint8, device=DEV)
+    with pytest.raises(pg.Pgf8Error):
+        pg.fp8_quantize_blocks(x, q=q)
+    _done()
+    assert bool((q == 7).all())
