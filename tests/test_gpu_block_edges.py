@@ -269,3 +269,77 @@ def test_quantize_row_groups_refuses_a_misaligned_batch_before_any_launch():
         pg.fp8_quantize_blocks(x, q=q)
     _done()
     assert bool((q == 7).all())
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+def test_quantize_tiles_nan_and_infinity(dt):
+    """128 x 128 blocks with NaNs, infinities and the ends of the range, whole
+    and ragged: NaN is ignored by the scale and keeps its code, an infinity
+    gives the infinite scale, zeros with their sign beside it."""
+    x = torch.randn((300, 400), generator=torch.Generator().manual_seed(4)).to(DT[dt])
+    x[5, 7] = float("nan")
+    x[130, 140] = float("inf")
+    x[131, 141] = float("nan")
+    x[140:150, 130] = -float("inf")
+    x[290, 260] = float("nan")
+    x[299, 399] = -float("inf")
+    x[:128, 384:] = float("nan")                      # nothing but NaN: the scale of zeros
+    x[256:, :128] = torch.finfo(DT[dt]).max
+    q, s = (_np(t) for t in pg.fp8_quantize_blocks(x.to(DEV), block_rows=128))
+    _done()
+    v = x.float().numpy()
+    for i in range(3):
+        for j in range(4):
+            at = np.s_[i * 128:(i + 1) * 128, j * 128:(j + 1) * 128]
+            b = v[at]
+            a = np.float32(np.abs(b[~np.isnan(b)]).max(initial=0.0))
+            want = a / np.float32(448) if a else np.float32(1)
+            assert s[i, j] == want, (i, j)
+            with np.errstate(all="ignore"):
+                r = oracle.e4m3_encode_array((b / want).astype(np.float32))
+            nan = np.isnan(b / want) if np.isfinite(want) else np.isnan(b) | np.isinf(b)
+            assert np.array_equal((q[at] & 0x7F) == 0x7F, nan), (i, j)
+            assert np.array_equal(q[at][~nan], r[~nan]), (i, j)
+
+
+@pytest.mark.parametrize("T", [1, 4, 20, 64])
+def test_moe_overlapping_the_kernels_around_it(T):
+    """Layers one after another, each launch overlapping the one before: the
+    router's input of a layer is the output of the last, the workspace, ids and
+    weights the same buffers, equal to the calls one by one."""
+    E, k, H, F, layers = 12, 3, 528, 272, 3
+    g = torch.Generator(device=DEV).manual_seed(T)
+    w = []
+    for _ in range(layers):
+        w13, s13 = pg.fp8_quantize_blocks(torch.randn((2 * E, F, H), generator=g, device=DEV) * 0.06, block_rows=128)
+        w2, s2 = pg.fp8_quantize_blocks(torch.randn((E, H, F), generator=g, device=DEV) * 0.06, block_rows=128)
+        wo, so = pg.fp8_quantize_blocks(torch.randn((H, H), generator=g, device=DEV) * 0.06, block_rows=128)
+        w.append((w13.view(E, 2 * F, H), s13.view(E, 2, up(F), up(H)), w2, s2, wo, so))
+    x0 = torch.randn((T, H), generator=g, device=DEV)
+    logits = torch.randn((layers, T, E), generator=g, device=DEV)
+
+    def step(flags, ws, wl, ids, wt, a, b):
+        a.copy_(x0)
+        for lay, (w13, s13, w2, s2, wo, so) in enumerate(w):
+            pg.fp8_block_linear_dynamic(a, wo, so, y=b, workspace=wl, flags=flags)
+            pg.fp8_moe(b, w13, s13, w2, s2, logits=logits[lay], top_k=k, y=a, ids=ids, weights=wt, workspace=ws,
+                       flags=flags)
+        return a.clone()
+
+    def buffers():
+        return (torch.empty(pg.fp8_moe_workspace_size(T, H, F, E, k), dtype=torch.uint8, device=DEV),
+                torch.empty(pg.fp8_block_linear_dynamic_workspace_size(T, H), dtype=torch.uint8, device=DEV),
+                torch.empty((T, k), dtype=torch.int32, device=DEV), torch.empty((T, k), device=DEV),
+                torch.empty((T, H), device=DEV), torch.empty((T, H), device=DEV))
+    want = step(0, *buffers())
+    b = buffers()
+    got = [step(pg.FLAG_OVERLAP_PREVIOUS, *b) for _ in range(5)]
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        out = step(pg.FLAG_OVERLAP_PREVIOUS, *b)
+    for _ in range(3):
+        graph.replay()
+    _done()
+    assert bool(torch.isfinite(want).all()) and bool((want != 0).any())
+    assert all(torch.equal(t, want) for t in got) and torch.equal(out, want)
