@@ -317,9 +317,15 @@ constexpr int kBlockFusedTokens = 4;
 // The layer from unquantised activations in one launch; the same codes, scales
 // and sums as in two.  False where a CTA's k-blocks would not fit its shared
 // memory, where y lies over x, and beyond 32 (token, k-block) groups a CTA, two
-// for each eight of its epilogue threads: the weights wait for them (12288 x
-// 4096, us on the GPU: one token, 16 groups, 12.6 in one launch and 13.3 in two;
-// two tokens 13.6 and 13.8; four tokens, 64 groups, 14.9 and 13.9).
+// for each eight of its epilogue threads: the weights wait for them.  Us on the
+// GPU in one launch / two, by groups a CTA (N x K, bf16):
+//   up to 32:  4096 x 4096 7.4 / 8.1 (1 token), 7.8 / 8.5 (4);
+//              1024 x 8192 7.4 / 8.2, 7.8 / 8.2; 4096 x 11008 11.2 / 12.8 (1), 12.2 /
+//              13.3 (2); 12288 x 4096 12.8 / 13.6, 13.6 / 14.0; 8192 x 8192 14.5 / 15.8,
+//              15.4 / 15.9
+//   33 to 44:  4096 x 11008 12.8 / 13.5 (3), 13.0 / 13.5 (4)
+//   48 to 64:  12288 x 4096 14.3 / 14.1 (3), 15.0 / 14.2 (4); 8192 x 8192 16.3 / 16.0, 16.9
+//              / 16.0
 static bool block_fused_launch(const BlockLaunch &L, int xdt, pgf8_status &st)
 {
     using B = BlockCfg<16, 6, 4>;

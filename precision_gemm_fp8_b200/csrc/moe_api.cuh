@@ -91,11 +91,18 @@ static pgf8_status launch_moe(void (*kernel)(Args...), dim3 grid, int threads, i
     return e == cudaSuccess ? PGF8_OK : cuda_fail(e);
 }
 
-// kb_us: see stream_plan (two weight tiles a k-block here).  The choice is flat
-// for gate+up (one token, 64 experts of 2048 x 1408, us of the layer at splits
-// of 1, 2, 3, 4, 6: 24.6, 23.3, 23.8, 23.9, 28.9; 64 tokens, 128 experts of 2048 x
-// 768: 189 at 1, 212 at 2) and steep for down (64 tokens: 259, 183, 189 at 2, 4,
-// 8, where 16 clusters of 8 do not fit at once; 140 at the 6 that it takes).
+// kb_us: see stream_plan (two weight tiles a k-block here).  Us of the layer with
+// one of the two kernels' splits set and the other's as chosen:
+//                                        gate+up 1    2    3    4    6   takes
+//   one token, 64 experts of 2048 x 1408     22.9 21.0 21.4 21.9 26.2    4
+//   13 tokens, 8 experts of 4096 x 7184       119  126  122  130  146    1
+//   30 tokens, 64 experts of 2048 x 1408      105  104  117  126  157    1
+//   64 tokens, 128 experts of 2048 x 768      139  163  206  235  310    1
+//                                        down    1    2    3    4    6    8   takes
+//   one token                                39.9 30.5 25.6 24.0 22.3 21.7    8
+//   13 tokens                                 230  160  142  130  119  118    8
+//   30 tokens                                 331  202  155  136  117  106    8
+//   64 tokens (16 clusters of 8 do not fit)   389  237  188  164  139  170    6
 template <class C>
 static pgf8_status launch_moe_up(const CUtensorMap &tmX, const CUtensorMap &tmW, const MoeUpParams &p, int most,
                                  double kb_us, cudaStream_t cs)
@@ -219,7 +226,7 @@ pgf8_status pgf8_fp8_moe(const pgf8_fp8_moe_layer *layer, int32_t flags, void *s
         st = launch_moe_up<MoeUpCfg<16, 3, 4, 2>>(tmX, tmW13, up, most, 0.40, cs);
     else if (bn == 32)
         st = launch_moe_up<MoeUpCfg<32, 3, 4, 2>>(tmX, tmW13, up, most, 0.45, cs);
-    else   // one CTA to an SM: at two, with 96 registers a thread, 64 tokens of 128 experts took 205 us against 166
+    else   // one CTA to an SM: two have 96 registers a thread and two ring stages (64 tokens of 128 experts: 185 us against 139)
         st = launch_moe_up<MoeUpCfg<64, 5, 2, 1>>(tmX, tmW13, up, most, 0.60, cs);
     if (st != PGF8_OK)
         return st;
