@@ -748,7 +748,9 @@ size_t pgf8_fp8_block_linear_dynamic_scales_offset(int64_t M, int64_t K);
  *         top_k] and weights [tokens, top_k] receive the choices, largest
  *         logit first (-1 and 0 where too few can be chosen); either may be
  *         NULL.  A logit of +inf gives the NaN weights that its softmax has.
- *         Without logits (NULL) ids and weights are read.  An id outside
+ *         Without logits (NULL) ids and weights are read; top_k is 1..16,
+ *         whatever experts is (the workspace of a call with more choices than
+ *         experts is that of top_k experts).  An id outside
  *         [0, experts) leaves its slot out (padding, another rank's expert); an
  *         expert that a token names twice counts with both weights.
  * A token without any expert gets y = 0.

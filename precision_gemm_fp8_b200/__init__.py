@@ -1033,7 +1033,8 @@ def fp8_moe(x: torch.Tensor, w13: torch.Tensor, s13: torch.Tensor, w2: torch.Ten
 
     Routing: from logits [T, E] and top_k (score MOE_SOFTMAX or MOE_SIGMOID,
     renormalised over the choices or not, times factor), or from given ids
-    int32 [T, k] and weights f32 [T, k] (ids outside [0, E) are left out).
+    int32 [T, k] and weights f32 [T, k] (ids outside [0, E) are left out: a
+    rank's experts may be fewer than the choices).
     Returns (y [T, H], ids, weights)."""
     if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
         raise ValueError("x must be [T, H] with contiguous rows")
@@ -1070,7 +1071,7 @@ def fp8_moe(x: torch.Tensor, w13: torch.Tensor, s13: torch.Tensor, w2: torch.Ten
             ids = x.new_empty((T, top_k), dtype=torch.int32)
         if weights is None:
             weights = x.new_empty((T, top_k), dtype=torch.float32)
-        workspace, nbytes = _workspace(workspace, lib.pgf8_fp8_moe_workspace_size(T, H, F, E, top_k), x)
+        workspace, nbytes = _workspace(workspace, lib.pgf8_fp8_moe_workspace_size(T, H, F, max(E, top_k), top_k), x)
         layer = MoeLayer(x.data_ptr(), w13.data_ptr(), s13.data_ptr(), w2.data_ptr(), s2.data_ptr(),
                          None if logits is None else logits.data_ptr(), ids.data_ptr(), weights.data_ptr(),
                          y.data_ptr(), workspace.data_ptr(), nbytes, T, H, F, E, top_k,

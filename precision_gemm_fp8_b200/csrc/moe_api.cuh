@@ -30,9 +30,10 @@ struct MoeWorkspace {
     }
 };
 
-static pgf8_status check_moe_sizes(int64_t T, int64_t H, int64_t F, int64_t E, int64_t K)
+// given: ids and weights are given, of which any number may lie outside the experts.
+static pgf8_status check_moe_sizes(int64_t T, int64_t H, int64_t F, int64_t E, int64_t K, bool given)
 {
-    if (T < 0 || H < 16 || F < 16 || E < 1 || K < 1 || K > E)
+    if (T < 0 || H < 16 || F < 16 || E < 1 || K < 1 || (K > E && !given))
         return PGF8_ERR_INVALID_ARG;
     if (T > kMoeMaxTokens || E > kMoeMaxExperts || K > kMoeMaxTopK || H > (1 << 20) || F > (1 << 20) ||
         2 * E * F > 2147483647ll - 128 || E * H > 2147483647ll - 128)
@@ -44,7 +45,7 @@ static pgf8_status check_moe_sizes(int64_t T, int64_t H, int64_t F, int64_t E, i
 
 static pgf8_status check_moe(const pgf8_fp8_moe_layer &a)
 {
-    pgf8_status st = check_moe_sizes(a.tokens, a.hidden, a.inter, a.experts, a.top_k);
+    pgf8_status st = check_moe_sizes(a.tokens, a.hidden, a.inter, a.experts, a.top_k, !a.logits);
     if (st != PGF8_OK)
         return st;
     if (a.score != kMoeSoftmax && a.score != kMoeSigmoid)
@@ -147,7 +148,7 @@ extern "C" {
 
 size_t pgf8_fp8_moe_workspace_size(int64_t tokens, int64_t hidden, int64_t inter, int64_t experts, int64_t top_k)
 {
-    if (tokens == 0 || check_moe_sizes(tokens, hidden, inter, experts, top_k) != PGF8_OK)
+    if (tokens == 0 || check_moe_sizes(tokens, hidden, inter, experts, top_k, false) != PGF8_OK)
         return 0;
     return MoeWorkspace(tokens, hidden, inter, experts, top_k).bytes;
 }

@@ -343,3 +343,33 @@ def test_moe_overlapping_the_kernels_around_it(T):
     _done()
     assert bool(torch.isfinite(want).all()) and bool((want != 0).any())
     assert all(torch.equal(t, want) for t in got) and torch.equal(out, want)
+
+
+@pytest.mark.parametrize("T,E,k", [(1, 1, 2), (5, 2, 8), (40, 3, 16), (64, 15, 16)])
+def test_moe_ranks_of_fewer_experts_than_choices(T, E, k):
+    """Experts dealt over ranks: each call is given the same k choices a token,
+    relative to its own E experts, and the ranks' sums are the layer's."""
+    H, F, ranks = 272, 144, 3
+    g = np.random.default_rng(T)
+    q13, s13 = zip(*[encode(g.standard_normal((F, H)).astype(np.float32) * 0.05, 128) for _ in range(2 * E * ranks)])
+    q2, s2 = zip(*[encode(g.standard_normal((H, F)).astype(np.float32) * 0.05, 128) for _ in range(E * ranks)])
+    w = (np.stack(q13).reshape(E * ranks, 2 * F, H), np.stack(s13).reshape(E * ranks, 2, up(F), up(H)), np.stack(q2),
+         np.stack(s2))
+    x = g.standard_normal((T, H)).astype(np.float32)
+    ids = np.stack([g.integers(0, E * ranks, k) for _ in range(T)]).astype(np.int32)      # some twice
+    wt = g.random((T, k)).astype(np.float32)
+    for r in range(ranks):
+        mine = tuple(t[r * E:(r + 1) * E] for t in w)
+        y, _, _ = pg.fp8_moe(_to(x), *(_to(t) for t in mine), ids=_to(ids - r * E), weights=_to(wt),
+                             out_dtype=torch.float32)
+        _done()
+        ref, off = moe(x, *mine, ids - r * E, wt)
+        err = np.abs(_np(y).astype(np.float64) - ref)
+        assert np.all(err <= off + 2.0 ** -24 * (np.abs(ref) + off) + 2.0 ** -150)
+
+
+def test_moe_more_choices_than_experts_need_given_ids():
+    w13, s13 = torch.zeros((2, 256, 128), dtype=torch.uint8, device=DEV), torch.ones((2, 2, 1, 1), device=DEV)
+    w2, s2 = torch.zeros((2, 128, 128), dtype=torch.uint8, device=DEV), torch.ones((2, 1, 1), device=DEV)
+    with pytest.raises(pg.Pgf8Error):
+        pg.fp8_moe(torch.zeros((4, 128), device=DEV), w13, s13, w2, s2, logits=torch.zeros((4, 2), device=DEV), top_k=3)
