@@ -993,7 +993,8 @@ def fp8_block_linear_dynamic(x: torch.Tensor, wq: torch.Tensor, sw: torch.Tensor
                              out_dtype: torch.dtype = torch.bfloat16, workspace: torch.Tensor | None = None,
                              flags: int = 0, stream=None) -> torch.Tensor:
     """fp8_block_linear of x [M, K] (f32, f16 or bf16; rows may be strided),
-    quantised in the call with one scale per 1 x 128 group.  Without a workspace
+    quantised in the call with one scale per 1 x 128 group; y may be x's memory.
+    Without a workspace
     (fp8_block_linear_dynamic_workspace_size bytes) the call allocates one, on
     its stream."""
     if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):

@@ -227,7 +227,7 @@ pgf8_status pgf8_fp8_moe(const pgf8_fp8_moe_layer *layer, int32_t flags, void *s
         st = launch_moe_up<MoeUpCfg<16, 3, 4, 2>>(tmX, tmW13, up, most, 0.40, cs);
     else if (bn == 32)
         st = launch_moe_up<MoeUpCfg<32, 3, 4, 2>>(tmX, tmW13, up, most, 0.45, cs);
-    else   // one CTA to an SM: two have 96 registers a thread and two ring stages (64 tokens of 128 experts: 185 us against 139)
+    else   // one CTA to an SM: two have 96 registers a thread and two stages (64 tokens of 128 experts: 185 us, 139)
         st = launch_moe_up<MoeUpCfg<64, 5, 2, 1>>(tmX, tmW13, up, most, 0.60, cs);
     if (st != PGF8_OK)
         return st;
